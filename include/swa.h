@@ -420,6 +420,106 @@ swa_status swa_decode_noalloc(const void* q, const void* k_new, const void* v_ne
                               int B, int Hq, int Hkv, int head_dim, void* out,
                               int dtype, void* stream);
 
+/* ------------------------------------------- rotary positions with several axes
+ * The rotation of swa_attn_pre (pair i = elements 2i, 2i+1 of a head times a complex
+ * number of modulus 1) for token rows of any length whose positions the caller
+ * gives: q and k of a whole clip before swa_prefill, the new tokens of a decode
+ * step, an image's patches.  The pairs split into one band per axis, pairs[0] of
+ * axis 0 first, then pairs[1] of axis 1, ...; pair j of a band of n turns by
+ * pos[token][axis] * theta^(-j/n), as in swa_rope3d_table.  Pairs behind the bands
+ * are copied.  inverse != 0 turns by the opposite angle: R is orthogonal, so
+ * that is the gradient: dx = swa_rope_nd(dy, inverse).
+ *   x, y: [tokens, heads, head_dim] with token rows x_row_stride / y_row_stride
+ *         elements apart (heads and elements of a row contiguous); y = x with equal
+ *         strides works in place, otherwise no element of y may be one of x.
+ *   pos:  [tokens, axes] int32, device.   pairs: [axes], host.
+ * head_dim a multiple of 8 up to 256, 1 to 4 axes, dtype either.  Angles are formed
+ * in 64 bits, so far positions lose nothing; products in 32.  Errors: SWA_ERR_ARG
+ * (null or misaligned pointer, row stride not a multiple of 16 bytes, theta <= 1,
+ * axes outside 1..4), SWA_ERR_SHAPE (row stride below heads * head_dim, a negative
+ * band, more pairs than head_dim / 2), SWA_ERR_UNSUPPORTED (head_dim). */
+swa_status swa_rope_nd(const void* x, void* y, const int32_t* pos, long long tokens, int heads, int head_dim,
+                       long long x_row_stride, long long y_row_stride, int axes, const int32_t* pairs,
+                       double theta, int inverse, int dtype, void* stream);
+
+/* ------------------------------------------------- rolling cache in 8 bits
+ * The rolling token cache of swa_decode at half its size.  A row (one token, one KV
+ * head, head_dim elements of K or of V) is kept as e4m3 values x8 and one byte
+ * e + 127: x is about x8 * 2^e with e the least integer for which
+ * max|x| <= 448 * 2^e, within [-40, 40].  Values are rounded to nearest even; what
+ * lies above 448 * 2^40 becomes that, NaN stays NaN (and has no part in e).
+ *   k8, v8: [B, W, Hkv, head_dim] e4m3;  k_exp, v_exp: [B, Hkv, W] bytes.
+ *   pos: [B] int64 in device memory, read by the kernels (a captured call can be
+ *        replayed as positions advance); a negative one marks an idle row.
+ * swa_kv8_write quantises tokens k, v [B, T, Hkv, head_dim] into the slots
+ * (pos[b] + t) mod W; swa_kv8_read reads the tokens at positions pos[b] + t back
+ * into k, v.  count (device, [B] int32, may be null: T for all) says how many of the
+ * T tokens sequence b has (taken as 0 below 0 and as T above T); slots and rows
+ * behind them, and all of an idle row, are left as they were.  Of a run longer than W
+ * the last W tokens are kept.  dtype is that of k and v; head_dim 32, 64 or 128.
+ * Errors: SWA_ERR_ARG, SWA_ERR_SHAPE (B over 65535), SWA_ERR_UNSUPPORTED. */
+swa_status swa_kv8_write(const void* k, const void* v, void* k8, uint8_t* k_exp, void* v8, uint8_t* v_exp,
+                         const long long* pos, const int32_t* count, int B, int T, int W, int Hkv, int head_dim,
+                         int dtype, void* stream);
+swa_status swa_kv8_read(const void* k8, const uint8_t* k_exp, const void* v8, const uint8_t* v_exp,
+                        const long long* pos, const int32_t* count, void* k, void* v, int B, int T, int W, int Hkv,
+                        int head_dim, int dtype, void* stream);
+
+/* ---------------------------------- decode steps with a position per sequence
+ * swa_decode's step (the new token's K/V into slot pos mod W, then its query heads
+ * attend to the valid slots, softmax scale 1/sqrt(head_dim)) with pos[b] for each
+ * sequence, int64 in device memory: slots 0..min(pos[b], W-1) are valid.  pos[b] < 0
+ * marks an idle row: its cache stays as it is, its output is zero.  A step can be
+ * captured into a graph and replayed as pos, q, k_new and v_new change in place.
+ *   q, out: [B, Hq, head_dim]; k_new, v_new: [B, Hkv, head_dim];
+ *   caches [B, W, Hkv, head_dim], updated in place; other slots are not written, and
+ *   slots behind the valid ones may hold anything, NaN included.
+ *   workspace: device scratch of the matching _workspace_bytes (0 for sizes that the
+ *   step refuses), 16-byte aligned; calls that share one must not overlap on the GPU.
+ * bf16: head_dim 64 or 128 with Hq/Hkv from 1 to 8; f32: head_dim 32, 64 or 128, any
+ * Hq/Hkv.  Errors: SWA_ERR_ARG, SWA_ERR_SHAPE (Hq not a multiple of Hkv, or sizes
+ * past the limits: Hq 65535, B * Hq 2^26), SWA_ERR_UNSUPPORTED, SWA_ERR_CAPACITY
+ * (workspace too small).
+ *
+ * swa_decode_kv8: on the 8-bit cache above; the new token is quantised as it is
+ * written and attended to as it is stored.  q and out are dtype.
+ *
+ * swa_decode_prefix: every sequence attends to the N tokens k_prefix, v_prefix
+ * [N, Hkv, head_dim] as well (a shared prompt or document, or retained first
+ * frames), which are kept once for the batch, and read once per group of rows,
+ * not once per sequence.  N may be 0.
+ *
+ * swa_decode_sparse: attends to n_select blocks of ``block`` slots (16, 32, 64 or
+ * 128) that a score chooses for each (sequence, KV head): of the ceil(n / block)
+ * blocks with valid slots the first n_first, the n_last newest (the block of the new
+ * token and those before it, cyclically in a full buffer), then those with the
+ * greatest sum over the group's query heads g and the elements d of
+ * max(q[g,d] low[d], q[g,d] high[d]) (the sum over the heads of a bound on the
+ * scores in the block), ties to the lower block; all of them where there are no more
+ * than n_select.  bounds [B, Hkv, ceil(W / block), 2, head_dim] (dtype) holds each
+ * block's elementwise lowest and highest key; the step renews the block that the
+ * token enters, and swa_block_bounds forms all of them from a cache whose newest
+ * positions are pos (NaN elements are passed over; a block without valid slots gets
+ * zeros and is never read).  selected [B, Hkv, n_select]: the chosen blocks in
+ * ascending order, -1 behind them.  Needs n_first + n_last <= n_select and
+ * B * Hkv <= 65535 (else SWA_ERR_SHAPE). */
+size_t swa_decode_kv8_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W);
+swa_status swa_decode_kv8(const void* q, const void* k_new, const void* v_new, void* k8, uint8_t* k_exp, void* v8,
+                          uint8_t* v_exp, const long long* pos, int W, int B, int Hq, int Hkv, int head_dim,
+                          void* out, void* workspace, size_t workspace_bytes, int dtype, void* stream);
+size_t swa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W, int N);
+swa_status swa_decode_prefix(const void* q, const void* k_new, const void* v_new, const void* k_prefix,
+                             const void* v_prefix, int N, void* k_cache, void* v_cache, const long long* pos, int W,
+                             int B, int Hq, int Hkv, int head_dim, void* out, void* workspace,
+                             size_t workspace_bytes, int dtype, void* stream);
+size_t swa_decode_sparse_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W, int block);
+swa_status swa_decode_sparse(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                             void* bounds, const long long* pos, int W, int block, int n_select, int n_first,
+                             int n_last, int B, int Hq, int Hkv, int head_dim, void* out, int32_t* selected,
+                             void* workspace, size_t workspace_bytes, int dtype, void* stream);
+swa_status swa_block_bounds(const void* k_cache, const long long* pos, void* bounds, int W, int block, int B,
+                            int Hkv, int head_dim, int dtype, void* stream);
+
 /* Diagnostic: y[i] = 2^x[i] as the attention kernels' FMA-pipe polynomial computes it
  * (Cody-Waite reduction + fitted cubic, relative error <= 8e-5 for x >= -125), for
  * n float32 device values.  Lets tests compare it with the hardware exp2. */

@@ -97,6 +97,17 @@ _sigs = {
     "swa_decode": (_i, [_vp, _vp, _vp, _vp, _vp, C.c_longlong, _i, _i, _i, _i, _i, _vp, _vp, _sz,
                         _i, _vp]),
     "swa_decode_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, C.c_longlong, _i, _i, _i, _i, _i, _vp, _i, _vp]),
+    "swa_rope_nd": (_i, [_vp, _vp, _vp, C.c_longlong, _i, _i, C.c_longlong, C.c_longlong, _i, _vp, C.c_double, _i,
+                         _i, _vp]),
+    "swa_kv8_write": (_i, [_vp] * 8 + [_i] * 6 + [_vp]),
+    "swa_kv8_read": (_i, [_vp] * 8 + [_i] * 6 + [_vp]),
+    "swa_decode_kv8_workspace_bytes": (_sz, [_i] * 5),
+    "swa_decode_kv8": (_i, [_vp] * 8 + [_i] * 5 + [_vp, _vp, _sz, _i, _vp]),
+    "swa_decode_prefix_workspace_bytes": (_sz, [_i] * 6),
+    "swa_decode_prefix": (_i, [_vp] * 5 + [_i] + [_vp] * 3 + [_i] * 5 + [_vp, _vp, _sz, _i, _vp]),
+    "swa_decode_sparse_workspace_bytes": (_sz, [_i] * 6),
+    "swa_decode_sparse": (_i, [_vp] * 7 + [_i] * 9 + [_vp, _vp, _vp, _sz, _i, _vp]),
+    "swa_block_bounds": (_i, [_vp] * 3 + [_i] * 6 + [_vp]),
     "swa_launch_count": (C.c_uint64, []),
     "swa_device_error_check": (_i, [_vp]),
     "swa_debug_wait_timeout": (_i, [_i, _vp]),
@@ -300,6 +311,197 @@ def swa_decode_noalloc(q, k_new, v_new, k_cache, v_cache, pos: int, out, stream=
                                    W, B, Hq, Hkv, D, _ptr(out), _dtype_code(q), _stream(stream)),
            "swa_decode_noalloc")
     return out
+
+
+# ------------------------------------ rotary positions with several axes
+def _cuda(*tensors) -> torch.device:
+    """The CUDA device that all the tensors are on."""
+    dev = tensors[0].device
+    if dev.type != "cuda" or any(t.device != dev for t in tensors):
+        raise ValueError(f"tensors must be on one CUDA device, got {[str(t.device) for t in tensors]}")
+    return dev
+
+
+def _like(what: str, t, shape, dtype) -> None:
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what}: want {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _token_rows(what: str, t) -> tuple[int, int]:
+    """(tokens, elements between them) of t [..., heads, head_dim] whose rows are
+    contiguous and whose leading axes step evenly from token to token."""
+    H, D = t.shape[-2:]
+    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    n, step = 1, H * D
+    for size, stride in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if size == 1:
+            continue
+        if n == 1:
+            step = stride
+        elif stride != n * step:
+            raise ValueError(f"{what}: tokens must be evenly spaced")
+        n *= size
+    return (0 if 0 in t.shape[:-2] else n), step
+
+
+def swa_rope_nd(x, pos, pairs, theta: float = 10000.0, inverse: bool = False, out=None, stream=None) -> torch.Tensor:
+    """Rotary positions with several axes: x [..., heads, head_dim] (token rows may be
+    a slice of wider ones) turned by int32 positions pos [..., axes], ``pairs[a]``
+    element pairs for axis a.  ``out`` may be x itself.  The gradient of the rotation
+    is the call with ``inverse=True`` on the output's gradient (see include/swa.h)."""
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    dev = _cuda(x, pos, out)
+    _like("pos", pos, tuple(x.shape[:-2]) + (len(pairs),), torch.int32)
+    _like("out", out, x.shape, x.dtype)
+    H, D = x.shape[-2:]
+    (n, xs), (_, ys) = _token_rows("x", x), _token_rows("out", out)
+    with torch.cuda.device(dev):
+        _check(_lib.swa_rope_nd(x.data_ptr(), out.data_ptr(), _ptr(pos), n, H, D, xs, ys, len(pairs),
+                                (C.c_int32 * max(1, len(pairs)))(*pairs), float(theta), int(bool(inverse)),
+                                _dtype_code(x), _stream(stream)), "swa_rope_nd")
+    return out
+
+
+# ------------------------------------------------- rolling cache in 8 bits
+def _cache8(k8, k_exp, v8, v_exp) -> tuple[int, int, int, int]:
+    B, W, Hkv, D = k8.shape
+    _like("k8", k8, (B, W, Hkv, D), torch.float8_e4m3fn)
+    _like("v8", v8, (B, W, Hkv, D), torch.float8_e4m3fn)
+    _like("k_exp", k_exp, (B, Hkv, W), torch.uint8)
+    _like("v_exp", v_exp, (B, Hkv, W), torch.uint8)
+    return B, W, Hkv, D
+
+
+def _run8(fn, name, k, v, k8, k_exp, v8, v_exp, pos, count, stream, write):
+    B, W, Hkv, D = _cache8(k8, k_exp, v8, v_exp)
+    T = k.shape[1] if k.dim() == 4 else -1
+    _like("k", k, (B, T, Hkv, D), k.dtype)
+    _like("v", v, (B, T, Hkv, D), k.dtype)
+    _like("pos", pos, (B,), torch.int64)
+    if count is not None:
+        _like("count", count, (B,), torch.int32)
+    dev = _cuda(k, v, k8, k_exp, v8, v_exp, pos, *([] if count is None else [count]))
+    cache = [_ptr(k8), _ptr(k_exp), _ptr(v8), _ptr(v_exp)]
+    run = [_ptr(k), _ptr(v)]
+    at = [_ptr(pos), _ptr(count)]
+    with torch.cuda.device(dev):
+        _check(fn(*(run + cache + at if write else cache + at + run), B, T, W, Hkv, D, _dtype_code(k),
+                  _stream(stream)), name)
+
+
+def swa_kv8_write(k, v, k8, k_exp, v8, v_exp, pos, count=None, stream=None) -> None:
+    """Quantise tokens k, v [B, T, Hkv, D] into the 8-bit rolling cache at positions
+    pos[b] + t (k8, v8 [B, W, Hkv, D] float8_e4m3fn, k_exp, v_exp [B, Hkv, W] uint8;
+    pos [B] int64, count [B] int32 or None; see include/swa.h)."""
+    _run8(_lib.swa_kv8_write, "swa_kv8_write", k, v, k8, k_exp, v8, v_exp, pos, count, stream, True)
+
+
+def swa_kv8_read(k8, k_exp, v8, v_exp, pos, k, v, count=None, stream=None):
+    """Read the tokens at positions pos[b] + t back from the 8-bit cache into k, v
+    [B, T, Hkv, D]; rows behind count[b] are left as they were."""
+    _run8(_lib.swa_kv8_read, "swa_kv8_read", k, v, k8, k_exp, v8, v_exp, pos, count, stream, False)
+    return k, v
+
+
+# ---------------------------------- decode steps with a position per sequence
+def swa_decode_kv8_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, W: int) -> int:
+    return int(_lib.swa_decode_kv8_workspace_bytes(B, Hq, Hkv, head_dim, W))
+
+
+def swa_decode_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, W: int, N: int) -> int:
+    return int(_lib.swa_decode_prefix_workspace_bytes(B, Hq, Hkv, head_dim, W, N))
+
+
+def swa_decode_sparse_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, W: int, block: int) -> int:
+    return int(_lib.swa_decode_sparse_workspace_bytes(B, Hq, Hkv, head_dim, W, block))
+
+
+def _step_args(q, k_new, v_new, pos, out, Hkv: int, *caches):
+    """Checks what the decode steps have in common; (device, B, Hq, D)."""
+    B, Hq, D = q.shape
+    _like("k_new", k_new, (B, Hkv, D), q.dtype)
+    _like("v_new", v_new, (B, Hkv, D), q.dtype)
+    _like("pos", pos, (B,), torch.int64)
+    _like("out", out, (B, Hq, D), q.dtype)
+    return _cuda(q, k_new, v_new, pos, out, *caches), B, Hq, D
+
+
+def _scratch(workspace, nbytes: int, dev, stream):
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        if stream is not None:  # the memory may not be handed on before that stream is through with it
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(int(stream), device=dev))
+        return workspace
+    if workspace.device != dev:
+        raise ValueError("workspace is on another device")
+    return workspace
+
+
+def swa_decode_kv8(q, k_new, v_new, k8, k_exp, v8, v_exp, pos, out, workspace=None, stream=None):
+    """One token per sequence at pos[b] on the 8-bit rolling cache (layouts as
+    swa_kv8_write), which is updated in place; q, out [B, Hq, D] (see include/swa.h)."""
+    Bc, W, Hkv, Dc = _cache8(k8, k_exp, v8, v_exp)
+    dev, B, Hq, D = _step_args(q, k_new, v_new, pos, out, Hkv, k8, k_exp, v8, v_exp)
+    _like("k8", k8, (B, W, Hkv, D), torch.float8_e4m3fn)
+    with torch.cuda.device(dev):
+        workspace = _scratch(workspace, swa_decode_kv8_workspace_bytes(B, Hq, Hkv, D, W), dev, stream)
+        _check(_lib.swa_decode_kv8(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k8), _ptr(k_exp), _ptr(v8), _ptr(v_exp),
+                                   _ptr(pos), W, B, Hq, Hkv, D, _ptr(out), _ptr(workspace), workspace.nbytes,
+                                   _dtype_code(q), _stream(stream)), "swa_decode_kv8")
+    return out
+
+
+def swa_decode_prefix(q, k_new, v_new, k_prefix, v_prefix, k_cache, v_cache, pos, out, workspace=None, stream=None):
+    """One token per sequence at pos[b] of its own rolling cache [B, W, Hkv, D], all of
+    them behind the shared prefix [N, Hkv, D] (see include/swa.h)."""
+    W, Hkv = k_cache.shape[1:3]
+    dev, B, Hq, D = _step_args(q, k_new, v_new, pos, out, Hkv, k_cache, v_cache, k_prefix, v_prefix)
+    N = k_prefix.shape[0]
+    for what, t, shape in (("k_cache", k_cache, (B, W, Hkv, D)), ("v_cache", v_cache, (B, W, Hkv, D)),
+                           ("k_prefix", k_prefix, (N, Hkv, D)), ("v_prefix", v_prefix, (N, Hkv, D))):
+        _like(what, t, shape, q.dtype)
+    with torch.cuda.device(dev):
+        workspace = _scratch(workspace, swa_decode_prefix_workspace_bytes(B, Hq, Hkv, D, W, N), dev, stream)
+        _check(_lib.swa_decode_prefix(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_prefix), _ptr(v_prefix), N,
+                                      _ptr(k_cache), _ptr(v_cache), _ptr(pos), W, B, Hq, Hkv, D, _ptr(out),
+                                      _ptr(workspace), workspace.nbytes, _dtype_code(q), _stream(stream)),
+               "swa_decode_prefix")
+    return out
+
+
+def swa_decode_sparse(q, k_new, v_new, k_cache, v_cache, bounds, pos, out, selected, block: int, n_first: int = 1,
+                      n_last: int = 1, workspace=None, stream=None):
+    """One token per sequence at pos[b] over the selected.shape[-1] cache blocks that a
+    score chooses per (sequence, KV head); ``selected`` [B, Hkv, n_select] int32
+    receives them, ``bounds`` [B, Hkv, ceil(W / block), 2, D] is kept up (see
+    include/swa.h and swa_block_bounds)."""
+    W, Hkv = k_cache.shape[1:3]
+    dev, B, Hq, D = _step_args(q, k_new, v_new, pos, out, Hkv, k_cache, v_cache, bounds, selected)
+    for what, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _like(what, t, (B, W, Hkv, D), q.dtype)
+    _like("bounds", bounds, (B, Hkv, -(-W // max(1, block)), 2, D), q.dtype)
+    _like("selected", selected, (B, Hkv, selected.shape[-1]), torch.int32)
+    with torch.cuda.device(dev):
+        workspace = _scratch(workspace, swa_decode_sparse_workspace_bytes(B, Hq, Hkv, D, W, block), dev, stream)
+        _check(_lib.swa_decode_sparse(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(bounds),
+                                      _ptr(pos), W, block, selected.shape[-1], n_first, n_last, B, Hq, Hkv, D,
+                                      _ptr(out), _ptr(selected), _ptr(workspace), workspace.nbytes, _dtype_code(q),
+                                      _stream(stream)), "swa_decode_sparse")
+    return out
+
+
+def swa_block_bounds(k_cache, pos, bounds, block: int, stream=None) -> torch.Tensor:
+    """Elementwise lowest and highest key of every block of a cache [B, W, Hkv, D] whose
+    newest positions are pos, for swa_decode_sparse."""
+    B, W, Hkv, D = k_cache.shape
+    _like("pos", pos, (B,), torch.int64)
+    _like("bounds", bounds, (B, Hkv, -(-W // max(1, block)), 2, D), k_cache.dtype)
+    with torch.cuda.device(_cuda(k_cache, pos, bounds)):
+        _check(_lib.swa_block_bounds(_ptr(k_cache), _ptr(pos), _ptr(bounds), W, block, B, Hkv, D,
+                                     _dtype_code(k_cache), _stream(stream)), "swa_block_bounds")
+    return bounds
 
 
 # ----------------------------------------------------------------- errors

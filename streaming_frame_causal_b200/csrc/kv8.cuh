@@ -1,0 +1,96 @@
+// kv8.cuh -- the 8-bit form of cached rows.  A row x[D] of one token and KV head
+// is held as e4m3 values and one exponent e: x is about x8 * 2^e, with e the least
+// integer for which max|x| <= 448 * 2^e (448 is the largest e4m3 value), kept
+// within [kE8Min, kE8Max] and stored as the byte e + 127.
+//
+// Scales are powers of two: a floating type gains nothing from the last fraction
+// of its range, x * 2^-e and x8 * 2^e are then exact, and so the only rounding is
+// e4m3's own (half a step, 2^-4 relative, for elements down to 2^-6 * 2^e).  A row
+// read back into 16 bits loses nothing more, and the products of the decode can
+// take the stored bytes as they are and apply 2^e to their 32-bit sums.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "ptx.cuh"
+
+namespace swa {
+
+constexpr int kE8Min = -40, kE8Max = 40;
+
+// e of a row whose largest magnitude is a (a >= 0, not NaN; infinity counts as
+// larger than everything)
+SWA_DEV int kv8_exponent(float a) {
+  const uint32_t u = __float_as_uint(a);
+  // a = 1.f * 2^(field - 127); 448 = 1.75 * 2^8
+  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, kE8Min), kE8Max);
+}
+
+// 2^e for e in the normal range
+SWA_DEV float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// two values to e4m3, rounded to nearest even; what is larger than 448 (an infinity
+// too) becomes 448, NaN stays NaN
+SWA_DEV uint32_t to_e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// two e4m3 values, exactly
+SWA_DEV float2 from_e4m3x2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// eight consecutive elements of a row in 32 bits
+SWA_DEV void load8(const float* x, float* v) {
+  const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+SWA_DEV void load8(const __nv_bfloat16* x, float* v) {
+  const uint4 a = *reinterpret_cast<const uint4*>(x);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+SWA_DEV void store8(float* x, const float* v) {
+  reinterpret_cast<float4*>(x)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(x)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+SWA_DEV void store8(__nv_bfloat16* x, const float* v) {
+  *reinterpret_cast<uint4*>(x) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// largest magnitude of eight elements (NaN passed over)
+SWA_DEV float amax8(const float* v) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
+  return a;
+}
+
+SWA_DEV uint2 quantise8(const float* v, int e) {
+  const float s = pow2i(-e);
+  return make_uint2(to_e4m3x2(v[0] * s, v[1] * s) | to_e4m3x2(v[2] * s, v[3] * s) << 16,
+                    to_e4m3x2(v[4] * s, v[5] * s) | to_e4m3x2(v[6] * s, v[7] * s) << 16);
+}
+
+SWA_DEV void dequantise8(uint2 q, int e, float* v) {
+  const float s = pow2i(e);
+  const uint32_t w[4] = {q.x, q.x >> 16, q.y, q.y >> 16};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = from_e4m3x2(w[i]);
+    v[2 * i] = f.x * s;
+    v[2 * i + 1] = f.y * s;
+  }
+}
+
+}  // namespace swa

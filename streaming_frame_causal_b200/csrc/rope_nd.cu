@@ -1,0 +1,190 @@
+// rope_nd.cu -- rotary positions with several axes on token rows of any length
+// (swa_rope_nd), and their gradient.
+//
+// Pair i of a head (elements 2i, 2i+1) belongs to one axis a and turns by
+// angle = pos[token][a] * theta^(-j / n_a), j its place among the axis' n_a pairs:
+// y = R(angle) x.  R is orthogonal, so the gradient with respect to x is the
+// rotation by -angle of the gradient with respect to y.
+//
+// Bound: device memory, x read once and y written once.  A token's angles are
+// the same for all its heads, so a block takes as many whole tokens as fill its
+// threads, forms their sines and cosines once in shared memory, and every thread
+// then rotates 16-byte pieces of the rows.  The first pieces are loaded before
+// the sines are formed, so that the loads are in flight meanwhile.  Angles are
+// formed and reduced to [-pi, pi] in 64 bits (a position of 10^6 times a rate of 1
+// has no fraction left in 32), the sine and cosine are taken in 32.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/swa.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace swa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeAhead = 4;       // 16-byte pieces a thread loads before the sines are formed
+constexpr int kRopeMaxPairs = 128;  // head_dim <= 256
+constexpr int kRopeMaxAxes = 4;
+constexpr int kRopeTablePairs = 2048;  // (token, pair) entries of a block's table
+
+struct RopeParams {
+  const uint8_t* x;
+  uint8_t* y;
+  const int* pos;           // [tokens, axes]
+  int64_t tokens;
+  int64_t x_row, y_row;     // bytes between token rows
+  int pieces;               // 16-byte pieces of a token's heads
+  int head_pieces;          // ... of one head
+  int pairs, axes;          // pairs that turn, of all axes together
+  int half;                 // head_dim / 2
+  int tokens_per_block;
+  int inverse;
+  int first[kRopeMaxAxes];  // first pair of each axis
+  double rate[kRopeMaxPairs];
+};
+
+// one 16-byte piece: E elements, E / 2 pairs, their (cos, sin) from t on
+template <typename T>
+SWA_DEV uint4 rotate_piece(uint4 v, const float2* t);
+
+template <>
+SWA_DEV uint4 rotate_piece<float>(uint4 v, const float2* t) {
+  const float4 c = *reinterpret_cast<const float4*>(t);
+  const float x0 = __uint_as_float(v.x), x1 = __uint_as_float(v.y);
+  const float x2 = __uint_as_float(v.z), x3 = __uint_as_float(v.w);
+  v.x = __float_as_uint(x0 * c.x - x1 * c.y);
+  v.y = __float_as_uint(x0 * c.y + x1 * c.x);
+  v.z = __float_as_uint(x2 * c.z - x3 * c.w);
+  v.w = __float_as_uint(x2 * c.w + x3 * c.z);
+  return v;
+}
+
+SWA_DEV uint32_t rotate_bf16x2(uint32_t v, float c, float s) {
+  const float x0 = __uint_as_float(v << 16), x1 = __uint_as_float(v & 0xffff0000u);
+  return pack_bf16x2(x0 * c - x1 * s, x0 * s + x1 * c);
+}
+
+template <>
+SWA_DEV uint4 rotate_piece<__nv_bfloat16>(uint4 v, const float2* t) {
+  const float4 a = *reinterpret_cast<const float4*>(t);
+  const float4 b = *reinterpret_cast<const float4*>(t + 2);
+  v.x = rotate_bf16x2(v.x, a.x, a.y);
+  v.y = rotate_bf16x2(v.y, a.z, a.w);
+  v.z = rotate_bf16x2(v.z, b.x, b.y);
+  v.w = rotate_bf16x2(v.w, b.z, b.w);
+  return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads) rope_nd_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kPairs = 16 / sizeof(T) / 2;  // pairs of a piece
+  __shared__ __align__(16) float2 table[kRopeTablePairs];
+  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tokens_per_block;
+  const int n_tok = static_cast<int>(p.tokens - tok0 < p.tokens_per_block ? p.tokens - tok0 : p.tokens_per_block);
+  const int n = n_tok * p.pieces;
+  const uint8_t* x = p.x + tok0 * p.x_row;
+  uint8_t* y = p.y + tok0 * p.y_row;
+  uint4 v[kRopeAhead];
+#pragma unroll
+  for (int k = 0; k < kRopeAhead; ++k) {
+    const int i = threadIdx.x + k * kRopeThreads;
+    if (i < n) {
+      const int tk = i / p.pieces;
+      v[k] = *reinterpret_cast<const uint4*>(x + tk * p.x_row + (i - tk * p.pieces) * 16);
+    }
+  }
+  for (int i = threadIdx.x; i < n_tok * p.half; i += kRopeThreads) {
+    const int tk = i / p.half, j = i - tk * p.half;
+    float2 cs = make_float2(1.f, 0.f);  // a pair behind the axes' stays as it is
+    if (j < p.pairs) {
+      int a = 0;
+      while (a + 1 < p.axes && j >= p.first[a + 1]) ++a;
+      constexpr double kTwoPi = 6.283185307179586476925, kInvTwoPi = 0.15915494309189533576889;
+      const double ang = static_cast<double>(__ldg(p.pos + (tok0 + tk) * p.axes + a)) * p.rate[j];
+      const float r = static_cast<float>(fma(-rint(ang * kInvTwoPi), kTwoPi, ang));
+      sincosf(r, &cs.y, &cs.x);
+      if (p.inverse) cs.y = -cs.y;
+    }
+    table[i] = cs;
+  }
+  __syncthreads();
+  auto put = [&](int i, uint4 u) {
+    const int tk = i / p.pieces, c = i - tk * p.pieces;
+    u = rotate_piece<T>(u, table + tk * p.half + (c % p.head_pieces) * kPairs);
+    *reinterpret_cast<uint4*>(y + tk * p.y_row + c * 16) = u;
+  };
+#pragma unroll
+  for (int k = 0; k < kRopeAhead; ++k) {
+    const int i = threadIdx.x + k * kRopeThreads;
+    if (i < n) put(i, v[k]);
+  }
+  for (int i = threadIdx.x + kRopeAhead * kRopeThreads; i < n; i += kRopeThreads) {
+    const int tk = i / p.pieces;
+    put(i, *reinterpret_cast<const uint4*>(x + tk * p.x_row + (i - tk * p.pieces) * 16));
+  }
+}
+
+}  // namespace
+}  // namespace swa
+
+extern "C" swa_status swa_rope_nd(const void* x, void* y, const int32_t* pos, long long tokens, int heads,
+                                  int head_dim, long long x_row_stride, long long y_row_stride, int axes,
+                                  const int32_t* pairs, double theta, int inverse, int dtype, void* stream) {
+  using namespace swa;
+  if (tokens < 0 || heads < 1 || head_dim < 1 || axes < 1 || axes > kRopeMaxAxes || !pairs || !(theta > 1.0) ||
+      !std::isfinite(theta))
+    return SWA_ERR_ARG;
+  if (dtype != SWA_F32 && dtype != SWA_BF16) return SWA_ERR_ARG;
+  if (head_dim % 8 || head_dim > 2 * kRopeMaxPairs) return SWA_ERR_UNSUPPORTED;
+  const int esize = dtype == SWA_BF16 ? 2 : 4;
+  const long long row = static_cast<long long>(heads) * head_dim;
+  if (row > (1 << 20) || x_row_stride < row || y_row_stride < row) return SWA_ERR_SHAPE;
+  if (x_row_stride > (1ll << 40) || y_row_stride > (1ll << 40) || tokens > (1ll << 40)) return SWA_ERR_SHAPE;
+  if (x_row_stride * esize % 16 || y_row_stride * esize % 16) return SWA_ERR_ARG;
+  RopeParams p{};
+  int n = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (pairs[a] < 0 || pairs[a] > head_dim / 2 - n) return SWA_ERR_SHAPE;
+    p.first[a] = n;
+    for (int j = 0; j < pairs[a]; ++j) p.rate[n++] = std::pow(theta, -static_cast<double>(j) / pairs[a]);
+  }
+  if (tokens == 0) return SWA_OK;
+  if (!x || !y || !pos) return SWA_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 15u) return SWA_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(pos) & 3u) return SWA_ERR_ARG;
+  int* err = nullptr;
+  if (const int ds = device_ready_status(&err)) return static_cast<swa_status>(ds);
+  p.x = static_cast<const uint8_t*>(x);
+  p.y = static_cast<uint8_t*>(y);
+  p.pos = pos;
+  p.tokens = tokens;
+  p.x_row = x_row_stride * esize;
+  p.y_row = y_row_stride * esize;
+  p.pieces = static_cast<int>(row * esize / 16);
+  p.head_pieces = head_dim * esize / 16;
+  p.pairs = n;
+  p.axes = axes;
+  p.half = head_dim / 2;
+  p.inverse = inverse != 0;
+  // whole tokens for about four pieces a thread, within the table, and not so many
+  // that SMs are left without a block
+  const int64_t fill = (kRopeAhead * kRopeThreads + p.pieces - 1) / p.pieces;
+  const int64_t spread = (tokens + 2 * device_sms() - 1) / (2 * device_sms());
+  p.tokens_per_block = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({fill, spread, kRopeTablePairs / p.half})));
+  const int64_t blocks = (tokens + p.tokens_per_block - 1) / p.tokens_per_block;
+  if (blocks > 0x7fffffffll) return SWA_ERR_SHAPE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == SWA_BF16)
+    rope_nd_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), kRopeThreads, 0, st>>>(p);
+  else
+    rope_nd_kernel<float><<<static_cast<unsigned>(blocks), kRopeThreads, 0, st>>>(p);
+  count_launches(1);
+  return cudaGetLastError() == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}

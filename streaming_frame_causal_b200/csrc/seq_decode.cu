@@ -1,0 +1,894 @@
+// seq_decode.cu -- decode steps in which every sequence has its own position: over
+// the 8-bit rolling cache (swa_decode_kv8), for a batch that shares a prefix
+// (swa_decode_prefix) and over blocks that a score selects (swa_decode_sparse).
+//
+// One step is a chain of kernels, each a programmatic dependent launch behind the
+// one before: the new token enters the cache and the work is divided (seq.cuh);
+// block-sparse: scores and selection; the prefix's pieces; the attention over the
+// caches; the merge of what was cut.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/swa.h"
+#include "internal.h"
+#include "kv8.cuh"
+#include "seq.cuh"
+
+namespace swa {
+namespace {
+
+enum SeqKind : int { SEQ_PLAIN = 0, SEQ_KV8 = 1 };
+
+SWA_DEV float to_f32(float v) { return v; }
+SWA_DEV float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+SWA_DEV void put_f32(float* p, float v) { *p = v; }
+SWA_DEV void put_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// ---------------------------------------------------------------- append and division
+// Block 0 divides the tiles; the warps of the other blocks take (sequence, KV head)
+// rows: the new token's K and V into slot pos mod W (as they are, or in 8 bits).
+// Block-sparse: the warp also renews the bounds of the block that the token entered,
+// from all its valid keys (the slot's old key may have been one of the extremes);
+// the new key comes from k_new, so nothing waits for the write above.
+constexpr int kPrepThreads = 256;
+constexpr int kPrepWarps = kPrepThreads / 32;
+
+template <typename T, int D, int KIND>
+__global__ void __launch_bounds__(kPrepThreads) seq_prep_kernel(const __grid_constant__ SeqParams p) {
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) {
+    __shared__ int sums[kPrepWarps + 1];
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
+      const int b = b0 + threadIdx.x;
+      const int v = b < p.B ? seq_tiles(p, b) : 0;
+      int s = v;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += y;
+      }
+      if (lane == 31) sums[warp] = s;
+      __syncthreads();
+      int before = carry, all = carry;
+      for (int w = 0; w < kPrepWarps; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+      }
+      if (b < p.B) p.cum[b] = before + s - v;
+      carry = all;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) p.cum[p.B] = carry;
+    __syncthreads();
+    const int64_t total = static_cast<int64_t>(carry) * p.items;
+    const int ctas = seq_ctas(p, total);
+    for (int c = threadIdx.x; c < p.ctas; c += kPrepThreads) {
+      int4 s = make_int4(0, 0, 0, 0);
+      if (c < ctas) {
+        const int64_t t = total * c / ctas, end = total * (c + 1) / ctas;
+        int lo = 0, hi = p.B;  // the last b whose tiles begin at t or before it
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (static_cast<int64_t>(p.cum[mid]) * p.items <= t) lo = mid;
+          else hi = mid;
+        }
+        const int of = p.cum[lo + 1] - p.cum[lo];
+        const int64_t r = t - static_cast<int64_t>(p.cum[lo]) * p.items;
+        s = make_int4(lo, static_cast<int>(r / of), static_cast<int>(r % of), static_cast<int>(end - t));
+      }
+      p.share[c] = s;
+    }
+    return;
+  }
+  constexpr int E = D / 32;  // elements of a lane
+  const int64_t row = static_cast<int64_t>(blockIdx.x - 1) * kPrepWarps + warp;
+  if (row >= static_cast<int64_t>(p.B) * p.Hkv) return;
+  const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<int64_t>(b) * p.Hkv);
+  const long long pos = p.pos[b];
+  if (pos < 0) return;
+  const int slot = static_cast<int>(pos % p.W);
+  const int64_t at = ((static_cast<int64_t>(b) * p.W + slot) * p.Hkv + h) * D + lane * E;
+  float kn[E];
+  for (int kv = 0; kv < 2; ++kv) {
+    const T* src = static_cast<const T*>(kv ? p.v_new : p.k_new) + row * D + lane * E;
+    float x[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = to_f32(src[i]);
+    if (kv == 0)
+#pragma unroll
+      for (int i = 0; i < E; ++i) kn[i] = x[i];
+    if constexpr (KIND == SEQ_KV8) {
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) a = fmaxf(a, fabsf(x[i]));
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+      const int e = kv8_exponent(a);
+      uint8_t* dst = static_cast<uint8_t*>(kv ? p.v_cache : p.k_cache) + at;
+#pragma unroll
+      for (int i = 0; i < E; ++i) dst[i] = static_cast<uint8_t>(to_e4m3x2(x[i] * pow2i(-e), 0.f));
+      if (lane == 0)
+        (kv ? p.v_exp : p.k_exp)[(static_cast<int64_t>(b) * p.Hkv + h) * p.W + slot] = static_cast<uint8_t>(e + 127);
+    } else {
+      T* dst = static_cast<T*>(kv ? p.v_cache : p.k_cache) + at;
+#pragma unroll
+      for (int i = 0; i < E; ++i) dst[i] = src[i];
+    }
+  }
+  if constexpr (KIND == SEQ_PLAIN) {
+    if (p.block == 0) return;
+    const int blk = slot / p.block, n = seq_tokens(p, b);
+    const int end = min(blk * p.block + p.block, n);
+    float lo[E], hi[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) lo[i] = hi[i] = kn[i];
+    const T* k = static_cast<const T*>(p.k_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + lane * E;
+#pragma unroll 8
+    for (int s = blk * p.block; s < end; ++s) {
+      if (s == slot) continue;
+      const T* r = k + static_cast<int64_t>(s) * p.Hkv * D;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float x = to_f32(r[i]);
+        lo[i] = fminf(lo[i], x);
+        hi[i] = fmaxf(hi[i], x);
+      }
+    }
+    T* o = static_cast<T*>(p.bounds) + (row * p.n_blocks + blk) * 2 * D + lane * E;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      put_f32(o + i, lo[i]);
+      put_f32(o + D + i, hi[i]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- block bounds of a whole cache
+template <typename T, int D>
+__global__ void __launch_bounds__(256) block_bounds_kernel(const SeqParams p) {
+  constexpr int E = D / 32;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // (b, block, head), heads fastest
+  const int lane = threadIdx.x & 31;
+  if (u >= static_cast<int64_t>(p.B) * p.n_blocks * p.Hkv) return;
+  const int64_t bj = u / p.Hkv;
+  const int h = static_cast<int>(u - bj * p.Hkv);
+  const int b = static_cast<int>(bj / p.n_blocks), j = static_cast<int>(bj - static_cast<int64_t>(b) * p.n_blocks);
+  const int end = min(j * p.block + p.block, seq_tokens(p, b));
+  float lo[E], hi[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    lo[i] = INFINITY;
+    hi[i] = -INFINITY;
+  }
+  const T* k = static_cast<const T*>(p.k_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + lane * E;
+#pragma unroll 8
+  for (int s = j * p.block; s < end; ++s) {
+    const T* r = k + static_cast<int64_t>(s) * p.Hkv * D;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float x = to_f32(r[i]);
+      lo[i] = fminf(lo[i], x);
+      hi[i] = fmaxf(hi[i], x);
+    }
+  }
+  if (j * p.block >= end) {  // an empty block's bounds are never read
+#pragma unroll
+    for (int i = 0; i < E; ++i) lo[i] = hi[i] = 0.f;
+  }
+  T* o = static_cast<T*>(p.bounds) + ((static_cast<int64_t>(b) * p.Hkv + h) * p.n_blocks + j) * 2 * D + lane * E;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    put_f32(o + i, lo[i]);
+    put_f32(o + D + i, hi[i]);
+  }
+}
+
+// ---------------------------------------------------------------- block scores
+// score(j) = sum over the group's query heads and the elements of max(q low_j, q high_j),
+// the sum over the heads of a bound that no key of the block exceeds.  With
+// up = sum_g max(q_g, 0) and down = sum_g min(q_g, 0) it is up . high_j + down . low_j,
+// two products per element whatever the group's size.  The sums are in 64 bits (two
+// more of them than the products of 16-bit values fill), so that blocks are ordered
+// as the definition orders them and only ties go to the lower index: in 32 bits two
+// near scores may change places, and with them what the step attends to.
+SWA_DEV uint64_t sortable(double x) {
+  if (isnan(x)) return 0;  // behind every number
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));  // -0 as +0
+  return (u >> 63) ? ~u : u | (1ull << 63);
+}
+
+constexpr int kScoreThreads = 256;
+constexpr int kScoreBlocks = 64;  // cache blocks of a CTA
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SeqParams p) {
+  griddep_launch_dependents();
+  constexpr int E = D / 32;
+  __shared__ double up[D], down[D];
+  const int64_t row = blockIdx.y;  // (b, KV head)
+  const int b = static_cast<int>(row / p.Hkv);
+  const int n = seq_tokens(p, b);
+  const int used = n > 0 ? (n + p.block - 1) / p.block : 0;
+  const T* q = static_cast<const T*>(p.q) + row * p.G * D;
+  if (threadIdx.x < D) {
+    double u = 0.0, d = 0.0;
+    for (int g = 0; g < p.G; ++g) {
+      const double x = static_cast<double>(to_f32(q[g * D + threadIdx.x]));
+      // a NaN fails both comparisons and goes to both sums
+      u += x < 0.0 ? 0.0 : x;
+      d += x > 0.0 ? 0.0 : x;
+    }
+    up[threadIdx.x] = u;
+    down[threadIdx.x] = d;
+  }
+  __syncthreads();
+  griddep_wait();  // the bounds of the newest block
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int newest = n > 0 ? static_cast<int>(p.pos[b] % p.W) / p.block : 0;
+  const int j0 = blockIdx.x * kScoreBlocks;
+  for (int j = j0 + warp; j < min(j0 + kScoreBlocks, used); j += kScoreThreads / 32) {
+    const T* r = static_cast<const T*>(p.bounds) + (row * p.n_blocks + j) * 2 * D + lane * E;
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      s += up[lane * E + i] * static_cast<double>(to_f32(r[D + i]));
+      s += down[lane * E + i] * static_cast<double>(to_f32(r[i]));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const int back = newest >= j ? newest - j : newest - j + used;
+    if (lane == 0) p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last) ? ~0ull : sortable(s);
+  }
+}
+
+// ---------------------------------------------------------------- selection
+// The n_select greatest scores of a row, ties to the lower index, their indices in
+// ascending order: the threshold is found a byte at a time from the top (a histogram
+// of the scores that agree with the bytes found so far), then one ordered pass
+// writes what is above it and the first of what equals it.
+constexpr int kSelThreads = 256;
+
+__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_constant__ SeqParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ int hist[256];
+  __shared__ int wsum[2][kSelThreads / 32];
+  __shared__ int s_bin, s_want;
+  const int64_t row = blockIdx.x;
+  const int b = static_cast<int>(row / p.Hkv);
+  const int n = seq_tokens(p, b);
+  const int used = n > 0 ? (n + p.block - 1) / p.block : 0;
+  int* sel = p.selected + row * p.n_select;
+  const int take = min(used, p.n_select);
+  for (int i = take + threadIdx.x; i < p.n_select; i += kSelThreads) sel[i] = -1;
+  if (used <= p.n_select) {
+    for (int i = threadIdx.x; i < used; i += kSelThreads) sel[i] = i;
+    return;
+  }
+  const uint64_t* score = p.score + row * p.n_blocks;
+  uint64_t found = 0, mask = 0;
+  int want = take;  // scores still to be found among those that agree with `found`
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int j = threadIdx.x; j < used; j += kSelThreads) {
+      const uint64_t s = score[j];
+      if ((s & mask) == found) atomicAdd(&hist[(s >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int bin = 255, left = want;
+      while (hist[bin] < left) left -= hist[bin--];
+      s_bin = bin;
+      s_want = left;
+    }
+    __syncthreads();
+    found |= static_cast<uint64_t>(s_bin) << shift;
+    mask |= 255ull << shift;
+    want = s_want;
+    __syncthreads();
+  }
+  // above: every score greater than the threshold; of those equal to it the first `want`
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int above = 0, equal = 0;  // so far, over all threads
+  for (int j0 = 0; j0 < used; j0 += kSelThreads) {
+    const int j = j0 + threadIdx.x;
+    const uint64_t s = j < used ? score[j] : 0;
+    const bool a = j < used && s > found, e = j < used && s == found;
+    const unsigned ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
+    if (lane == 0) {
+      wsum[0][warp] = __popc(ba);
+      wsum[1][warp] = __popc(be);
+    }
+    __syncthreads();
+    int xa = above + __popc(ba & ((1u << lane) - 1)), xe = equal + __popc(be & ((1u << lane) - 1));
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w < warp) {
+        xa += wsum[0][w];
+        xe += wsum[1][w];
+      }
+      above += wsum[0][w];
+      equal += wsum[1][w];
+    }
+    if (a || (e && xe < want)) sel[xa + min(xe, want)] = j;
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- attention on CUDA cores
+// 32-bit queries and outputs.  One 128-key tile at a time in shared memory as 32-bit
+// values (rows D + 4 apart, so that eight lanes' 16-byte reads fall on different
+// banks): a thread per key for the scores of up to 8 query heads, a warp per two
+// heads for the softmax, a thread per output element (and 128 / D parts of the keys)
+// for the weighted sum.
+constexpr int kSimtThreads = 128;
+
+template <int D>
+struct SimtPlan {
+  static constexpr int kLd = D + 4;
+  static constexpr int kTile = kSeqKeys * kLd;
+  static constexpr int kFloats = kTile + kSeqRows * kSeqKeys + kSeqRows * D + 3 * kSeqRows;
+  static constexpr int kSmem = kFloats * 4;
+};
+
+// rows [0, 128) of a tile: row r from slot[r] (behind the keys: zeros), times 2^exp for 8-bit rows
+template <typename T, int D, int KIND, typename Slot>
+SWA_DEV void simt_load(float* tile, const void* rows, int64_t row_elems, const uint8_t* exps, Slot slot_of) {
+  constexpr int kParts = D / 8;
+  for (int i = threadIdx.x; i < kSeqKeys * kParts; i += kSimtThreads) {
+    const int r = i / kParts, part = i - r * kParts;
+    const int slot = slot_of(r);
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (slot >= 0) {
+      if constexpr (KIND == SEQ_KV8) {
+        const uint2 u =
+            *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(rows) + slot * row_elems + part * 8);
+        dequantise8(u, exps[slot] - 127, v);
+      } else {
+        load8(static_cast<const T*>(rows) + slot * row_elems + part * 8, v);
+      }
+    }
+    store8(tile + r * SimtPlan<D>::kLd + part * 8, v);
+  }
+}
+
+// the running state of one item's rows
+template <typename T, int D>
+struct SimtState {
+  float acc[kSeqRows];
+  float *tile, *w, *q, *m, *l, *alpha;
+  SWA_DEV void bind(float* smem) {
+    tile = smem;
+    w = tile + SimtPlan<D>::kTile;
+    q = w + kSeqRows * kSeqKeys;
+    m = q + kSeqRows * D;
+    l = m + kSeqRows;
+    alpha = l + kSeqRows;
+  }
+  // q rows [0, rows) from src, the rest zero
+  SWA_DEV void begin(const T* src, int rows) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kSeqRows * D; i += kSimtThreads) {
+      const int r = i / D;
+      q[i] = r < rows ? to_f32(src[i]) : 0.f;
+    }
+    if (threadIdx.x < kSeqRows) {
+      m[threadIdx.x] = -INFINITY;
+      l[threadIdx.x] = 0.f;
+    }
+#pragma unroll
+    for (int h = 0; h < kSeqRows; ++h) acc[h] = 0.f;
+  }
+  // one tile: keys, then values, loaded by the two functions
+  template <typename LoadK, typename LoadV>
+  SWA_DEV void step(float scale_log2, bool valid, LoadK load_k, LoadV load_v) {
+    const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
+    load_k();
+    __syncthreads();
+    float s[kSeqRows];
+#pragma unroll
+    for (int h = 0; h < kSeqRows; ++h) s[h] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      const float4 k = *reinterpret_cast<const float4*>(tile + r * SimtPlan<D>::kLd + d);
+#pragma unroll
+      for (int h = 0; h < kSeqRows; ++h) {
+        const float4 x = *reinterpret_cast<const float4*>(q + h * D + d);
+        s[h] += k.x * x.x + k.y * x.y + k.z * x.z + k.w * x.w;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < kSeqRows; ++h) w[h * kSeqKeys + r] = valid ? s[h] * scale_log2 : -INFINITY;
+    __syncthreads();
+    load_v();  // the keys are read
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int h = warp * 2 + hh;
+      float x[4], top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = w[h * kSeqKeys + lane + 32 * i];
+        top = fmaxf(top, x[i]);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const float m0 = m[h], m1 = fmaxf(m0, top);
+      const float ref = m1 == -INFINITY ? 0.f : m1;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = exp2f(x[i] - ref);
+        w[h * kSeqKeys + lane + 32 * i] = e;
+        sum += e;
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      __syncwarp();
+      if (lane == 0) {
+        const float al = exp2f(m0 - ref);
+        alpha[h] = al;
+        l[h] = l[h] * al + sum;
+        m[h] = m1;
+      }
+    }
+    __syncthreads();
+    constexpr int kParts = kSimtThreads / D;  // parts of the keys
+    const int d = r % D, part = r / D;
+#pragma unroll
+    for (int h = 0; h < kSeqRows; ++h) acc[h] *= alpha[h];
+#pragma unroll 4
+    for (int i = part * (kSeqKeys / kParts); i < (part + 1) * (kSeqKeys / kParts); ++i) {
+      const float v = tile[i * SimtPlan<D>::kLd + d];
+#pragma unroll
+      for (int h = 0; h < kSeqRows; ++h) acc[h] += w[h * kSeqKeys + i] * v;
+    }
+    __syncthreads();
+  }
+  // hands (head, element, sum over the keys, maximum, sum of the weights) to put
+  template <typename Put>
+  SWA_DEV void end(int rows, Put put) {
+    constexpr int kParts = kSimtThreads / D;
+    const int d = threadIdx.x % D, part = threadIdx.x / D;
+    if (kParts > 1) {
+#pragma unroll
+      for (int h = 0; h < kSeqRows; ++h) tile[(part * kSeqRows + h) * D + d] = acc[h];
+      __syncthreads();
+    }
+    if (part == 0) {
+      for (int h = 0; h < rows; ++h) {
+        float o = acc[0];
+        if (kParts > 1) {
+          o = 0.f;
+          for (int i = 0; i < kParts; ++i) o += tile[(i * kSeqRows + h) * D + d];
+        } else {
+#pragma unroll
+          for (int i = 1; i < kSeqRows; ++i)
+            if (i == h) o = acc[i];
+        }
+        put(h, d, o, m[h], l[h]);
+      }
+    }
+  }
+};
+
+template <typename T, int D, int KIND>
+__global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_constant__ SeqParams p) {
+  extern __shared__ __align__(16) float smem[];
+  griddep_launch_dependents();
+  griddep_wait();
+  SimtState<T, D> st;
+  st.bind(smem);
+  SeqWalk walk;
+  walk.start(p, blockIdx.x);
+  SeqRun run;
+  while (walk.next(p, blockIdx.x, run)) {
+    const int kvh = run.item / p.groups, g0 = (run.item - kvh * p.groups) * kSeqRows;
+    const int rows = min(kSeqRows, p.G - g0);
+    const int64_t qrow = static_cast<int64_t>(run.b) * p.Hq + kvh * p.G + g0;
+    const int n = seq_tokens(p, run.b);
+    st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
+    const int64_t row_elems = static_cast<int64_t>(p.Hkv) * D;
+    const int64_t base = (static_cast<int64_t>(run.b) * p.W * p.Hkv + kvh) * D;
+    const int64_t ebase = (static_cast<int64_t>(run.b) * p.Hkv + kvh) * p.W;
+    for (int t = run.t0; t < run.t0 + run.tiles; ++t) {
+      auto slot = [&](int r) { return seq_slot(p, run.b, kvh, n, t, r); };
+      auto load = [&](const void* cache, const uint8_t* exps) {
+        const uint8_t* rows8 = static_cast<const uint8_t*>(cache) + base * (KIND == SEQ_KV8 ? 1 : sizeof(T));
+        simt_load<T, D, KIND>(st.tile, rows8, row_elems, KIND == SEQ_KV8 ? exps + ebase : nullptr, slot);
+      };
+      st.step(p.scale_log2, slot(threadIdx.x) >= 0, [&] { load(p.k_cache, p.k_exp); },
+              [&] { load(p.v_cache, p.v_exp); });
+    }
+    st.end(rows, [&](int h, int d, float o, float m, float l) {
+      if (run.slot < 0) {
+        put_f32(static_cast<T*>(p.out) + (qrow + h) * D + d, o / l);
+      } else {
+        const int64_t at = static_cast<int64_t>(run.slot) * kSeqRows + h;
+        p.part_o[at * D + d] = o;
+        if (d == 0) {
+          p.part_ml[at * 2] = m;
+          p.part_ml[at * 2 + 1] = l;
+        }
+      }
+    });
+  }
+}
+
+// the shared prefix: 8 of the batch's rows of a KV head against a piece of it
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_constant__ SeqParams p) {
+  extern __shared__ __align__(16) float smem[];
+  griddep_launch_dependents();
+  griddep_wait();  // the one before may still read the partials of an earlier step
+  SimtState<T, D> st;
+  st.bind(smem);
+  const int kvh = blockIdx.y, split = blockIdx.z;
+  const int64_t rows_all = static_cast<int64_t>(p.B) * p.groups;
+  const int64_t rg = blockIdx.x;  // (sequence, group of its heads)
+  if (rg >= rows_all) return;
+  const int b = static_cast<int>(rg / p.groups), g0 = static_cast<int>(rg - static_cast<int64_t>(b) * p.groups) * kSeqRows;
+  if (p.pos[b] < 0) return;
+  const int rows = min(kSeqRows, p.G - g0);
+  const int64_t qrow = static_cast<int64_t>(b) * p.Hq + kvh * p.G + g0;
+  const int tiles = (p.N + kSeqKeys - 1) / kSeqKeys;
+  const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
+  const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits);
+  st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
+  for (int t = t0; t < t1; ++t) {
+    auto slot = [&](int r) { return t * kSeqKeys + r < p.N ? t * kSeqKeys + r : -1; };
+    auto load = [&](const void* x) {
+      simt_load<T, D, SEQ_PLAIN>(st.tile, static_cast<const T*>(x) + kvh * D, static_cast<int64_t>(p.Hkv) * D,
+                                 nullptr, slot);
+    };
+    st.step(p.scale_log2, slot(threadIdx.x) >= 0, [&] { load(p.k_prefix); }, [&] { load(p.v_prefix); });
+  }
+  st.end(rows, [&](int h, int d, float o, float m, float l) {
+    const int64_t at = static_cast<int64_t>(split) * p.B * p.Hq + qrow + h;
+    p.pre_o[at * D + d] = o;
+    if (d == 0) {
+      p.pre_ml[at * 2] = m;
+      p.pre_ml[at * 2 + 1] = l;
+    }
+  });
+}
+
+// ---------------------------------------------------------------- merge
+// One warp per (sequence, query head): sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over
+// the pieces of its item, in the order of the tiles, then the prefix's.  Items that
+// one CTA held whole are written already; an idle row's output is zero.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) seq_merge_kernel(const __grid_constant__ SeqParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int E = D / 32;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (u >= static_cast<int64_t>(p.B) * p.Hq) return;
+  const int b = static_cast<int>(u / p.Hq), h = static_cast<int>(u - static_cast<int64_t>(b) * p.Hq);
+  const int kvh = h / p.G, g = h - kvh * p.G;
+  const int item = kvh * p.groups + g / kSeqRows, row = g % kSeqRows;
+  T* out = static_cast<T*>(p.out) + u * D + lane * E;
+  const int tiles = p.cum[b + 1] - p.cum[b];
+  if (tiles == 0) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) put_f32(out + i, 0.f);
+    return;
+  }
+  const int64_t total = static_cast<int64_t>(p.cum[p.B]) * p.items;
+  const int64_t t = static_cast<int64_t>(p.cum[b]) * p.items + static_cast<int64_t>(item) * tiles;
+  const int ctas = seq_ctas(p, total);
+  const int c0 = seq_owner(t, total, ctas), c1 = seq_owner(t + tiles - 1, total, ctas);
+  if (c0 == c1 && p.N == 0) return;
+  const int pieces = c1 - c0 + 1;
+  auto part = [&](int i, const float*& o, float& m, float& l) {
+    const float* ml;
+    if (i < pieces) {
+      const int64_t slot = pieces == 1 ? 2 * p.ctas + static_cast<int64_t>(b) * p.items + item
+                                       : (i == 0 ? 2 * c0 + 1 : 2 * (c0 + i));
+      o = p.part_o + (slot * kSeqRows + row) * D + lane * E;
+      ml = p.part_ml + (slot * kSeqRows + row) * 2;
+    } else {
+      const int64_t at = static_cast<int64_t>(i - pieces) * p.B * p.Hq + u;
+      o = p.pre_o + at * D + lane * E;
+      ml = p.pre_ml + at * 2;
+    }
+    m = ml[0];
+    l = ml[1];
+  };
+  float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0.f;
+  const int all = pieces + p.splits;
+  const float* o;
+  float m, l;
+  for (int i = 0; i < all; ++i) {
+    part(i, o, m, l);
+    M = fmaxf(M, m);
+  }
+  for (int i = 0; i < all; ++i) {
+    part(i, o, m, l);
+    const float w = exp2f(m - M);
+    L += w * l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += w * o[e];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) put_f32(out + e, acc[e] / L);
+}
+
+
+// ---------------------------------------------------------------- host
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// The device buffers of a step inside the caller's workspace, in this order.
+struct SeqLayout {
+  size_t cum, share, part_o, part_ml, pre_o, pre_ml, score, bytes;
+};
+
+// Pieces of the prefix for the CUDA-core kernel: enough for three CTAs per SM.
+int prefix_pieces(const SeqParams& p) {
+  if (p.N == 0) return 0;
+  const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.Hkv;
+  const int64_t want = (3 * 148 + ctas - 1) / ctas;
+  const int tiles = cdiv(p.N, kSeqKeys);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, tiles, kSeqMaxSplits})));
+}
+
+SeqLayout seq_layout(const SeqParams& p, int D) {
+  SeqLayout l{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
+  const size_t slots = 2 * kSeqMaxCtas + (p.N > 0 ? static_cast<size_t>(p.B) * p.items : 0);
+  const size_t pre = static_cast<size_t>(p.splits) * p.B * p.Hq;
+  l.cum = take((static_cast<size_t>(p.B) + 1) * sizeof(int));
+  l.share = take(kSeqMaxCtas * sizeof(int4));
+  l.part_o = take(slots * kSeqRows * D * sizeof(float));
+  l.part_ml = take(slots * kSeqRows * 2 * sizeof(float));
+  l.pre_o = take(pre * D * sizeof(float));
+  l.pre_ml = take(pre * 2 * sizeof(float));
+  l.score = take(p.block ? static_cast<size_t>(p.B) * p.Hkv * p.n_blocks * sizeof(uint64_t) : 0);
+  l.bytes = at;
+  return l;
+}
+
+// Sizes that every entry point refuses or accepts alike; fills the derived ones.
+swa_status seq_sizes(SeqParams& p, int D, int dtype) {
+  if (p.W < 1 || p.B < 0 || p.Hq < 1 || p.Hkv < 1 || D < 1 || p.N < 0) return SWA_ERR_ARG;
+  if (dtype != SWA_F32 && dtype != SWA_BF16) return SWA_ERR_ARG;
+  if (p.Hq % p.Hkv) return SWA_ERR_SHAPE;
+  p.G = p.Hq / p.Hkv;
+  if (dtype == SWA_BF16 && ((D != 64 && D != 128) || p.G > 8)) return SWA_ERR_UNSUPPORTED;
+  if (dtype == SWA_F32 && D != 32 && D != 64 && D != 128) return SWA_ERR_UNSUPPORTED;
+  p.groups = cdiv(p.G, kSeqRows);
+  p.items = p.Hkv * p.groups;
+  if (p.Hq > 65535 || static_cast<int64_t>(p.B) * p.Hq > (1ll << 26) ||
+      static_cast<int64_t>(p.B) * (p.W / kSeqKeys + 2) > 0x7fffffffll)
+    return SWA_ERR_SHAPE;
+  p.splits = prefix_pieces(p);
+  return SWA_OK;
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, DeviceOnce& once) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  if (once.done(dev)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) once.mark(dev);
+  return e;
+}
+
+template <typename T, int D, int KIND>
+cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
+  p.ctas = std::min(3 * device_sms(), kSeqMaxCtas);
+  const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv;
+  seq_prep_kernel<T, D, KIND>
+      <<<static_cast<unsigned>(1 + (rows + kPrepWarps - 1) / kPrepWarps), kPrepThreads, 0, st>>>(p);
+  int launches = 1;
+  cudaError_t e = cudaGetLastError();
+  if constexpr (KIND == SEQ_PLAIN) {
+    if (e == cudaSuccess && p.block) {
+      const dim3 grid(cdiv(p.n_blocks, kScoreBlocks), static_cast<unsigned>(rows));
+      e = launch_after(block_score_kernel<T, D>, grid, dim3(kScoreThreads), 0, st, p);
+      if (e == cudaSuccess)
+        e = launch_after(block_select_kernel, dim3(static_cast<unsigned>(rows)), dim3(kSelThreads), 0, st, p);
+      launches += 2;
+    }
+    if (e == cudaSuccess && p.N > 0) {
+      static DeviceOnce once;
+      e = allow_smem(prefix_simt_kernel<T, D>, SimtPlan<D>::kSmem, once);
+      const dim3 grid(static_cast<unsigned>(p.B * p.groups), p.Hkv, p.splits);
+      if (e == cudaSuccess)
+        e = launch_after(prefix_simt_kernel<T, D>, grid, dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
+      ++launches;
+    }
+  }
+  if (e == cudaSuccess) {
+    static DeviceOnce once;
+    e = allow_smem(seq_simt_kernel<T, D, KIND>, SimtPlan<D>::kSmem, once);
+    if (e == cudaSuccess)
+      e = launch_after(seq_simt_kernel<T, D, KIND>, dim3(p.ctas), dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
+    ++launches;
+  }
+  if (e == cudaSuccess) {
+    const int64_t heads = static_cast<int64_t>(p.B) * p.Hq;
+    e = launch_after(seq_merge_kernel<T, D>, dim3(static_cast<unsigned>((heads + 7) / 8)), dim3(256), 0, st, p);
+    ++launches;
+  }
+  count_launches(launches);
+  return e;
+}
+
+template <int KIND>
+cudaError_t launch_step_d(SeqParams& p, int D, int dtype, cudaStream_t st) {
+  if (dtype == SWA_BF16)
+    return D == 64 ? launch_step<__nv_bfloat16, 64, KIND>(p, st) : launch_step<__nv_bfloat16, 128, KIND>(p, st);
+  if (D == 32) return launch_step<float, 32, KIND>(p, st);
+  if (D == 64) return launch_step<float, 64, KIND>(p, st);
+  return launch_step<float, 128, KIND>(p, st);
+}
+
+template <int KIND>
+swa_status seq_step(SeqParams& p, int D, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!p.q || !p.k_new || !p.v_new || !p.k_cache || !p.v_cache || !p.pos || !p.out) return SWA_ERR_ARG;
+  if (!al16(p.q) || !al16(p.k_new) || !al16(p.v_new) || !al16(p.k_cache) || !al16(p.v_cache) || !al16(p.out) ||
+      !al16(p.k_prefix) || !al16(p.v_prefix) || !al16(p.bounds) || (reinterpret_cast<uintptr_t>(p.pos) & 7u) ||
+      (reinterpret_cast<uintptr_t>(p.selected) & 3u))
+    return SWA_ERR_ARG;
+  const SeqLayout l = seq_layout(p, D);
+  if (!workspace || workspace_bytes < l.bytes) return SWA_ERR_CAPACITY;
+  if (!al16(workspace)) return SWA_ERR_ARG;
+  if (const int ds = device_ready_status(&p.err)) return static_cast<swa_status>(ds);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.cum = reinterpret_cast<int*>(ws + l.cum);
+  p.share = reinterpret_cast<int4*>(ws + l.share);
+  p.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  p.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+  p.pre_o = reinterpret_cast<float*>(ws + l.pre_o);
+  p.pre_ml = reinterpret_cast<float*>(ws + l.pre_ml);
+  p.score = reinterpret_cast<uint64_t*>(ws + l.score);
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+  return launch_step_d<KIND>(p, D, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+SeqParams seq_params(const void* q, const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                     const long long* pos, int W, int B, int Hq, int Hkv, void* out) {
+  SeqParams p{};
+  p.q = q;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.pos = pos;
+  p.W = W;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.out = out;
+  return p;
+}
+
+bool block_size(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
+
+// the workspace of a step of these sizes: enough for either type
+size_t workspace_of(SeqParams p, int D) {
+  if (p.B < 1 || seq_sizes(p, D, SWA_F32) != SWA_OK) return 0;
+  return seq_layout(p, D).bytes;
+}
+
+}  // namespace
+}  // namespace swa
+
+using namespace swa;
+
+extern "C" size_t swa_decode_kv8_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W) {
+  return workspace_of(seq_params(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W, B, Hq, Hkv, nullptr), head_dim);
+}
+
+extern "C" size_t swa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W, int N) {
+  SeqParams p = seq_params(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W, B, Hq, Hkv, nullptr);
+  p.N = N;
+  return workspace_of(p, head_dim);
+}
+
+extern "C" size_t swa_decode_sparse_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W, int block) {
+  if (!block_size(block) || W < 1) return 0;
+  SeqParams p = seq_params(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W, B, Hq, Hkv, nullptr);
+  p.block = block;
+  p.n_blocks = cdiv(W, block);
+  return workspace_of(p, head_dim);
+}
+
+extern "C" swa_status swa_decode_kv8(const void* q, const void* k_new, const void* v_new, void* k8, uint8_t* k_exp,
+                                     void* v8, uint8_t* v_exp, const long long* pos, int W, int B, int Hq, int Hkv,
+                                     int head_dim, void* out, void* workspace, size_t workspace_bytes, int dtype,
+                                     void* stream) {
+  SeqParams p = seq_params(q, k_new, v_new, k8, v8, pos, W, B, Hq, Hkv, out);
+  if (const swa_status s = seq_sizes(p, head_dim, dtype)) return s;
+  if (B == 0) return SWA_OK;
+  if (!k_exp || !v_exp) return SWA_ERR_ARG;
+  p.k_exp = k_exp;
+  p.v_exp = v_exp;
+  return seq_step<SEQ_KV8>(p, head_dim, dtype, workspace, workspace_bytes, stream);
+}
+
+extern "C" swa_status swa_decode_prefix(const void* q, const void* k_new, const void* v_new, const void* k_prefix,
+                                        const void* v_prefix, int N, void* k_cache, void* v_cache,
+                                        const long long* pos, int W, int B, int Hq, int Hkv, int head_dim, void* out,
+                                        void* workspace, size_t workspace_bytes, int dtype, void* stream) {
+  SeqParams p = seq_params(q, k_new, v_new, k_cache, v_cache, pos, W, B, Hq, Hkv, out);
+  p.N = N;
+  if (const swa_status s = seq_sizes(p, head_dim, dtype)) return s;
+  if (B == 0) return SWA_OK;
+  if (N > 0 && (!k_prefix || !v_prefix)) return SWA_ERR_ARG;
+  p.k_prefix = k_prefix;
+  p.v_prefix = v_prefix;
+  return seq_step<SEQ_PLAIN>(p, head_dim, dtype, workspace, workspace_bytes, stream);
+}
+
+extern "C" swa_status swa_decode_sparse(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                                        void* v_cache, void* bounds, const long long* pos, int W, int block,
+                                        int n_select, int n_first, int n_last, int B, int Hq, int Hkv, int head_dim,
+                                        void* out, int32_t* selected, void* workspace, size_t workspace_bytes,
+                                        int dtype, void* stream) {
+  if (n_select < 1 || n_first < 0 || n_last < 0) return SWA_ERR_ARG;
+  SeqParams p = seq_params(q, k_new, v_new, k_cache, v_cache, pos, W, B, Hq, Hkv, out);
+  if (const swa_status s = seq_sizes(p, head_dim, dtype)) return s;
+  if (!block_size(block)) return SWA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n_first) + n_last > n_select || n_select > (1 << 20) ||
+      static_cast<int64_t>(B) * Hkv > 65535)
+    return SWA_ERR_SHAPE;
+  if (B == 0) return SWA_OK;
+  if (!bounds || !selected) return SWA_ERR_ARG;
+  p.bounds = bounds;
+  p.selected = selected;
+  p.block = block;
+  p.n_select = n_select;
+  p.n_first = n_first;
+  p.n_last = n_last;
+  p.n_blocks = cdiv(W, block);
+  return seq_step<SEQ_PLAIN>(p, head_dim, dtype, workspace, workspace_bytes, stream);
+}
+
+namespace {
+template <typename T, int D>
+cudaError_t launch_bounds_of(const SeqParams& p, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(p.B) * p.n_blocks * p.Hkv;
+  block_bounds_kernel<T, D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+}  // namespace
+
+extern "C" swa_status swa_block_bounds(const void* k_cache, const long long* pos, void* bounds, int W, int block, int B,
+                                       int Hkv, int head_dim, int dtype, void* stream) {
+  SeqParams p = seq_params(nullptr, nullptr, nullptr, const_cast<void*>(k_cache), nullptr, pos, W, B, Hkv, Hkv, nullptr);
+  if (const swa_status s = seq_sizes(p, head_dim, dtype)) return s;
+  if (!block_size(block)) return SWA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * Hkv > 65535) return SWA_ERR_SHAPE;
+  if (B == 0) return SWA_OK;
+  if (!k_cache || !pos || !bounds) return SWA_ERR_ARG;
+  if (!al16(k_cache) || !al16(bounds) || (reinterpret_cast<uintptr_t>(pos) & 7u)) return SWA_ERR_ARG;
+  if (const int ds = device_ready_status(&p.err)) return static_cast<swa_status>(ds);
+  p.bounds = bounds;
+  p.block = block;
+  p.n_blocks = cdiv(W, block);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == SWA_BF16)
+    e = head_dim == 64 ? launch_bounds_of<__nv_bfloat16, 64>(p, st) : launch_bounds_of<__nv_bfloat16, 128>(p, st);
+  else
+    e = head_dim == 32 ? launch_bounds_of<float, 32>(p, st)
+                       : head_dim == 64 ? launch_bounds_of<float, 64>(p, st) : launch_bounds_of<float, 128>(p, st);
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}

@@ -1,0 +1,278 @@
+"""Rotary positions with several axes, the 8-bit rolling cache and the decode steps
+with a position per sequence, against float64 (oracle/token_cache.py).
+
+Tolerances, element by element.  u = torch.finfo(dtype).eps / 2 is the largest
+relative error of a rounding to dtype.
+  rope    the output's rounding u |y|, and 2^-20 (|a| + |b|) for a pair (a, b): the angle
+          rounded to 32 bits (2^-22 up to pi), its sine and cosine (2 ulp), two products
+          and a sum (2^-24 each), 2^-21 for 64-bit angles of positions up to 2^31
+  decode  bf16: the output's rounding u |o|, the weights' rounding u * sum p|v| (a weight
+          may be held in 16 bits or in 9 significant ones, 2^-9 + 2^-11 < u; the sum of
+          the weights is not rounded, so an error of u in each is one of u in o / l), and
+          the scores' error: 2^-17 relative in the weights for 32-bit sums and exponentials
+          at scores below 2^6, and for queries held as two e4m3 terms an error of
+          2^-10 in units of the row's scale per element (max|q| > 224 units), hence
+          sum_d |k_d| max|q| 2^-17.8 / sqrt(D) in a score, times 2 in o (numerator and sum)
+          f32: 2^-15 sum p|v| (the same 32-bit sums and exponentials, sums over up to
+          2^13 keys)
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import token_cache as orc
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def swa():
+    import streaming_frame_causal_b200 as m
+    return m
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def randn(shape, seed, dtype, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (scale * torch.randn(shape, generator=g)).to(dtype).cuda()
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def check_decode(out, ref, scale, dtype, q=None, k=None, what=""):
+    got = np64(out)
+    assert np.isfinite(got).all(), what
+    if dtype == F32:
+        tol = 2.0 ** -15 * scale
+    else:
+        u = half_step(dtype)
+        tol = u * np.abs(ref) + u * scale + 2.0 ** -17 * scale
+        if q is not None:
+            ds = np.abs(q).max() * np.abs(k).sum(-1).max() * 2.0 ** -17.8 / np.sqrt(q.shape[-1])
+            tol = tol + 2 * ds * scale
+    bad = np.abs(got - ref) > tol + 1e-30
+    assert not bad.any(), f"{what}: {np.abs(got - ref)[bad].max()} off, {bad.mean():.4f} of the elements"
+
+
+# ------------------------------------------------------------------ rope
+@pytest.mark.parametrize("tokens,H,D,pairs,dtype", [
+    (1, 1, 64, (12, 10, 10), BF16),
+    (777, 5, 64, (12, 10, 10), BF16),
+    (130, 40, 128, (22, 21, 21), F32),
+    (33, 3, 256, (128,), BF16),            # one axis over the whole head
+    (50, 2, 96, (0, 7, 11, 3), F32),       # an axis without pairs, pairs left as they are
+    (9, 7, 8, (1, 2), BF16),
+    (5, 2, 16, (0, 0), F32),               # nothing turns
+    (3, 700, 128, (32, 16, 16), F32),      # a token wider than a block's first loads
+])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_matches_float64(swa, tokens, H, D, pairs, dtype, inverse):
+    x = randn((tokens, H, D), tokens + D, dtype)
+    g = torch.Generator().manual_seed(tokens)
+    pos = torch.randint(-1000, 2 ** 31 - 1, (tokens, len(pairs)), generator=g, dtype=torch.int64).to(torch.int32)
+    pos[0] = 0
+    y = swa.swa_rope_nd(x, pos.cuda(), pairs, inverse=inverse)
+    ref = orc.rope_nd(np64(x), pos.numpy().astype(np.int64), pairs, inverse=inverse)
+    size = np.abs(np64(x)).reshape(tokens, H, D // 2, 2).sum(-1).repeat(2, -1)
+    assert (np.abs(np64(y) - ref) <= half_step(dtype) * np.abs(ref) + 2.0 ** -20 * size).all()
+    assert torch.equal(y[..., 2 * sum(pairs):], x[..., 2 * sum(pairs):])
+
+
+def test_rope_in_place_on_slices_and_as_the_prologue_turns(swa):
+    # q and k heads of fused rows, in place: the rest of the rows stays
+    buf = randn((2, 37, 12, 64), 3, BF16)
+    keep = buf.clone()
+    t = torch.arange(37, dtype=torch.int32)
+    pos = torch.stack([t + 5, t // 6, t % 6], 1).repeat(2, 1, 1).cuda()
+    swa.swa_rope_nd(buf[:, :, :9], pos, (12, 10, 10), out=buf[:, :, :9])
+    apart = swa.swa_rope_nd(keep[:, :, :9], pos, (12, 10, 10))
+    assert apart.is_contiguous() and torch.equal(buf[:, :, :9], apart) and torch.equal(buf[:, :, 9:], keep[:, :, 9:])
+    # the same rotation as one frame's table: token k of frame 5, no special tokens, grid width 6
+    rot = np64(swa.swa_rope3d_table(5, 37, 0, 6, 64))
+    first = pos[0].clone()
+    first[:, 0] = 5
+    x = randn((37, 4, 64), 4, F32)
+    got = np64(swa.swa_rope_nd(x, first, (12, 10, 10)))
+    z = np64(x).reshape(37, 4, 32, 2)
+    want = (z[..., 0] + 1j * z[..., 1]) * (rot[..., 0] + 1j * rot[..., 1])[:, None]
+    np.testing.assert_allclose(got, np.stack([want.real, want.imag], -1).reshape(37, 4, 64), atol=2.0 ** -19)
+
+
+def test_rope_inverse_is_the_gradient(swa):
+    x, w = randn((19, 3, 64), 5, F32), randn((19, 3, 64), 6, F32)
+    pos = torch.randint(0, 500, (19, 3), dtype=torch.int32).cuda()
+    grad = np64(swa.swa_rope_nd(w, pos, (12, 10, 10), inverse=True))
+    f = lambda z: (orc.rope_nd(z, pos.cpu().numpy(), (12, 10, 10)) * np64(w)).sum()  # noqa: E731
+    x64 = np64(x)
+    for i in np.random.RandomState(0).randint(0, x64.size, 40):
+        d = np.zeros(x64.size)
+        d[i] = 0.5  # the rotation is linear: the difference is exact but for 64-bit sums
+        diff = f(x64 + d.reshape(x64.shape)) - f(x64 - d.reshape(x64.shape))
+        assert abs(diff - grad.flat[i]) <= 2.0 ** -20 * 2 * np.abs(np64(w)).max() + 1e-10
+
+
+# ------------------------------------------------------------------ 8-bit cache
+def new_cache8(B, W, Hkv, D):
+    """A cache whose unwritten slots hold NaN."""
+    return [torch.full((B, W, Hkv, D), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+            if i % 2 == 0 else torch.full((B, Hkv, W), 200, dtype=torch.uint8, device="cuda") for i in range(4)]
+
+
+def values8(x8, e):
+    """Stored rows in 64 bits [B, W, Hkv, D]."""
+    return np64(x8.float()) * 2.0 ** (np64(e).transpose(0, 2, 1)[..., None] - 127)
+
+
+@pytest.mark.parametrize("B,T,W,Hkv,D,dtype", [
+    (1, 1, 1, 1, 64, BF16), (3, 70, 64, 2, 128, BF16), (2, 33, 100, 3, 64, F32), (4, 5, 7, 1, 32, F32),
+    (2, 300, 40, 2, 32, BF16),
+])
+def test_kv8_write_and_read_back(swa, B, T, W, Hkv, D, dtype):
+    k, v = randn((B, T, Hkv, D), 1, dtype, 3.0), randn((B, T, Hkv, D), 2, dtype)
+    k *= torch.exp2(torch.randint(-60, 60, (B, T, Hkv, 1)).float()).to(dtype).cuda()  # past both ends of e
+    k[0, 0, 0] = 0.0
+    v[-1, -1, -1, 3] = 448.0 * 4  # a row whose largest element is the largest stored value
+    v[-1, -1, 0, 0] = float("inf")
+    v[0, T // 2, 0, 1] = float("nan")
+    v[0, T // 2, 0, 2] = -float("inf")
+    pos = torch.tensor([(7 * b * W) // 3 for b in range(B)])
+    count = torch.tensor([T - b for b in range(B)], dtype=torch.int32).clamp(min=-1)
+    if B > 2:
+        pos[1] = -1
+    cache = new_cache8(B, W, Hkv, D)
+    before = [t.clone() for t in cache]
+    swa.swa_kv8_write(k, v, *cache, pos.cuda(), count=count.cuda())
+    for x, (x8, e), (o8, oe) in ((k, cache[:2], before[:2]), (v, cache[2:], before[2:])):
+        val, ex = orc.quantise8(np64(x))
+        want8, wante = np64(o8.float()), oe.cpu().numpy().copy()
+        for b in range(B):
+            for t in range(max(0, int(count[b]))):
+                if pos[b] >= 0:
+                    want8[b, (int(pos[b]) + t) % W] = val[b, t]
+                    wante[b, :, (int(pos[b]) + t) % W] = ex[b, t] + 127
+        np.testing.assert_array_equal(np64(x8.float()), want8)
+        np.testing.assert_array_equal(e.cpu().numpy(), wante)
+    # back, the last min(T, W) tokens of each run; rows behind them stay
+    n = min(T, W)
+    start = pos + (count - n).clamp(min=0) * (pos >= 0)
+    for back in (BF16, F32):
+        kb, vb = (torch.full((B, n, Hkv, D), 7.0, dtype=back, device="cuda") for _ in range(2))
+        swa.swa_kv8_read(*cache, start.cuda(), kb, vb, count=count.cuda())
+        for x, (x8, e) in ((kb, cache[:2]), (vb, cache[2:])):
+            stored = values8(x8, e)
+            want = np.full((B, n, Hkv, D), 7.0)
+            for b in range(B):
+                for t in range(min(n, max(0, int(count[b])))):
+                    if pos[b] >= 0:
+                        want[b, t] = stored[b, (int(start[b]) + t) % W]
+            np.testing.assert_array_equal(np64(x), want)  # 4 significant bits and a power of two: exact in both
+
+
+# ------------------------------------------------------------------ decode steps
+def lengths(B, W, seed, idle=False):
+    g = np.random.RandomState(seed)
+    pos = g.randint(0, 3 * W, B)
+    pos[0] = 0
+    if B > 1:
+        pos[1] = W - 1
+    if B > 2:
+        pos[2] = g.randint(0, W)
+    if idle:
+        pos[-1] = -1
+    return torch.tensor(pos, dtype=torch.int64)
+
+
+STEP_CASES = [
+    (1, 1, 1, 1, 64, BF16), (1, 5, 2, 1, 128, BF16), (5, 300, 8, 2, 64, BF16), (4, 1000, 12, 4, 128, BF16),
+    (3, 129, 16, 2, 64, BF16), (2, 2600, 5, 1, 128, BF16), (70, 40, 2, 2, 64, BF16), (3, 257, 14, 2, 128, BF16),
+    (2, 700, 6, 1, 64, BF16), (6, 384, 7, 7, 128, BF16), (3, 200, 6, 2, 32, F32), (4, 333, 20, 2, 64, F32),
+    (2, 1500, 4, 4, 128, F32), (130, 20, 3, 1, 64, F32),
+]
+
+
+@pytest.mark.parametrize("B,W,Hq,Hkv,D,dtype", STEP_CASES)
+def test_decode_kv8_matches_float64(swa, B, W, Hq, Hkv, D, dtype):
+    pos = lengths(B, W, W, idle=B > 3)
+    q, kn, vn = (randn((B, h, D), s, dtype, z) for h, s, z in ((Hq, 1, 1.5), (Hkv, 2, 1.0), (Hkv, 3, 1.0)))
+    n = torch.clamp(pos + 1, 0, W)
+    cache = new_cache8(B, W, Hkv, D)
+    k, v = randn((B, W, Hkv, D), 4, dtype), randn((B, W, Hkv, D), 5, dtype, 5.0)
+    swa.swa_kv8_write(k, v, *cache, torch.zeros(B, dtype=torch.int64).cuda(), count=n.int().cuda())
+    kc, vc = values8(*cache[:2]), values8(*cache[2:])
+    new = [a * 2.0 ** e[..., None] for a, e in (orc.quantise8(np64(kn)), orc.quantise8(np64(vn)))]
+    ref, scale, kc, vc = orc.decode_step(np64(q), *new, kc, vc, pos.numpy())
+    out = torch.full_like(q, float("nan"))
+    swa.swa_decode_kv8(q, kn, vn, *cache, pos.cuda(), out)
+    torch.cuda.synchronize()
+    assert swa.swa_device_error_check() == 0
+    live = np.where(np.isnan(kc), 0.0, kc)
+    check_decode(out, ref, scale, dtype, np64(q), live, "kv8")
+    np.testing.assert_array_equal(values8(*cache[:2]), kc)
+    np.testing.assert_array_equal(values8(*cache[2:]), vc)
+
+
+def own_cache(B, W, Hkv, D, pos, dtype):
+    """Caches whose slots behind the valid ones hold NaN."""
+    k, v = randn((B, W, Hkv, D), 4, dtype), randn((B, W, Hkv, D), 5, dtype)
+    for b in range(B):
+        k[b, max(0, int(pos[b]) + 1):] = float("nan")
+        v[b, max(0, int(pos[b]) + 1):] = float("nan")
+    return k, v
+
+
+@pytest.mark.parametrize("N", [0, 1, 128, 1000])
+@pytest.mark.parametrize("B,W,Hq,Hkv,D,dtype", STEP_CASES)
+def test_decode_prefix_matches_float64(swa, B, W, Hq, Hkv, D, dtype, N):
+    pos = lengths(B, W, W + 1, idle=B > 3)
+    q, kn, vn = (randn((B, h, D), s, dtype, z) for h, s, z in ((Hq, 1, 1.5), (Hkv, 2, 1.0), (Hkv, 3, 1.0)))
+    k, v = own_cache(B, W, Hkv, D, pos, dtype)
+    kp, vp = randn((N, Hkv, D), 6, dtype), randn((N, Hkv, D), 7, dtype)
+    ref, scale, kc, vc = orc.decode_step(np64(q), np64(kn), np64(vn), np64(k), np64(v), pos.numpy(),
+                                         prefix=(np64(kp), np64(vp)))
+    out = torch.full_like(q, float("nan"))
+    swa.swa_decode_prefix(q, kn, vn, kp, vp, k, v, pos.cuda(), out)
+    torch.cuda.synchronize()
+    assert swa.swa_device_error_check() == 0
+    check_decode(out, ref, scale, dtype, what="prefix")
+    np.testing.assert_array_equal(np64(k), kc)
+    np.testing.assert_array_equal(np64(v), vc)
+
+
+@pytest.mark.parametrize("block,n_select,n_first,n_last", [(16, 3, 1, 1), (32, 1, 0, 0), (64, 7, 2, 3), (128, 2, 0, 2),
+                                                           (16, 40, 0, 1)])
+@pytest.mark.parametrize("B,W,Hq,Hkv,D,dtype", STEP_CASES)
+def test_decode_sparse_matches_float64(swa, B, W, Hq, Hkv, D, dtype, block, n_select, n_first, n_last):
+    pos = lengths(B, W, W + 2, idle=B > 3)
+    q, kn, vn = (randn((B, h, D), s, dtype, z) for h, s, z in ((Hq, 1, 1.5), (Hkv, 2, 1.0), (Hkv, 3, 1.0)))
+    k, v = own_cache(B, W, Hkv, D, pos, dtype)
+    if W >= 200:  # two blocks alike: equal scores, the lower one is taken
+        k[:, block:2 * block] = k[:, :max(0, min(block, W - block))]
+    before = torch.where(pos >= 0, pos - 1, pos)  # as the step before left them
+    bounds = torch.full((B, Hkv, -(-W // block), 2, D), float("nan"), dtype=dtype, device="cuda")
+    swa.swa_block_bounds(k, before.cuda(), bounds, block)
+    np.testing.assert_array_equal(np64(bounds), orc.block_bounds(np64(k), before.numpy(), block))
+    sel = torch.full((B, Hkv, n_select), 99, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    k0, v0 = np64(k), np64(v)
+    swa.swa_decode_sparse(q, kn, vn, k, v, bounds, pos.cuda(), out, sel, block, n_first=n_first, n_last=n_last)
+    torch.cuda.synchronize()
+    assert swa.swa_device_error_check() == 0
+    want_bounds = orc.block_bounds(np64(k), pos.numpy(), block)
+    np.testing.assert_array_equal(np64(bounds), want_bounds)
+    chosen = orc.select_blocks(np64(q), want_bounds, pos.numpy(), W, block, n_select, n_first, n_last)
+    want = np.full((B, Hkv, n_select), -1)
+    for b in range(B):
+        for h in range(Hkv):
+            want[b, h, :len(chosen[b][h])] = chosen[b][h]
+    np.testing.assert_array_equal(sel.cpu().numpy(), want)
+    ref, scale, kc, vc = orc.decode_step(np64(q), np64(kn), np64(vn), k0, v0, pos.numpy(), chosen=chosen, block=block)
+    check_decode(out, ref, scale, dtype, what="sparse")
+    np.testing.assert_array_equal(np64(k), kc)
+    np.testing.assert_array_equal(np64(v), vc)

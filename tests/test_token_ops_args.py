@@ -1,0 +1,142 @@
+"""Refusals of the token-cache operators, on the host: every bad call returns its
+status before anything is launched, and the binding refuses tensors that do not fit."""
+import ctypes as C
+
+import pytest
+import torch
+
+A = 256  # an aligned address that is never read
+ARG, SHAPE, CAPACITY, UNSUPPORTED = -1, -2, -4, -7
+
+
+@pytest.fixture(scope="module")
+def swa():
+    import __graft_entry__
+    __graft_entry__._builder().build()
+    import streaming_frame_causal_b200 as m
+    return m
+
+
+def rope(lib, x=A, y=A, pos=A, tokens=4, heads=2, D=64, xs=128, ys=128, pairs=(12, 10, 10), theta=1e4, dtype=1):
+    p = None if pairs is None else (C.c_int32 * max(1, len(pairs)))(*pairs)
+    return lib.swa_rope_nd(x, y, pos, tokens, heads, D, xs, ys, 0 if pairs is None else len(pairs), p, theta, 0, dtype,
+                           None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(tokens=-1), ARG), (dict(heads=0), ARG), (dict(D=0), ARG), (dict(pairs=None), ARG), (dict(pairs=()), ARG),
+    (dict(pairs=(1, 1, 1, 1, 1)), ARG), (dict(theta=1.0), ARG), (dict(theta=float("nan")), ARG),
+    (dict(theta=float("inf")), ARG), (dict(dtype=2), ARG), (dict(x=None), ARG), (dict(y=None), ARG),
+    (dict(pos=None), ARG), (dict(x=A + 8), ARG), (dict(y=A + 2), ARG), (dict(pos=A + 2), ARG),
+    (dict(xs=132), ARG), (dict(ys=129), ARG), (dict(xs=127), SHAPE), (dict(ys=64), SHAPE),
+    (dict(pairs=(-1, 2)), SHAPE), (dict(pairs=(12, 10, 11)), SHAPE), (dict(D=60, xs=128, ys=128), UNSUPPORTED),
+    (dict(D=264, xs=528, ys=528), UNSUPPORTED), (dict(tokens=0, x=None, y=None, pos=None), 0),
+])
+def test_rope_refusals(swa, bad, status):
+    assert rope(swa._lib, **bad) == status
+
+
+def run8(fn, ptr=(A,) * 7, count=None, B=2, T=3, W=8, Hkv=2, D=64, dtype=1):
+    return fn(*ptr, count, B, T, W, Hkv, D, dtype, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(B=-1), ARG), (dict(T=-1), ARG), (dict(W=0), ARG), (dict(Hkv=0), ARG), (dict(D=0), ARG), (dict(dtype=5), ARG),
+    (dict(D=96), UNSUPPORTED), (dict(B=65536), SHAPE), (dict(B=0, ptr=(None,) * 7), 0), (dict(T=0, ptr=(None,) * 7), 0),
+    *[(dict(ptr=tuple(None if i == j else A for i in range(7))), ARG) for j in range(7)],
+])
+@pytest.mark.parametrize("name", ["swa_kv8_write", "swa_kv8_read"])
+def test_kv8_run_refusals(swa, name, bad, status):
+    assert run8(getattr(swa._lib, name), **bad) == status
+
+
+@pytest.mark.parametrize("name,j", [("swa_kv8_write", 0), ("swa_kv8_write", 1), ("swa_kv8_write", 2), ("swa_kv8_write", 4),
+                                    ("swa_kv8_read", 0), ("swa_kv8_read", 2)])
+def test_kv8_run_refuses_misaligned_rows(swa, name, j):
+    assert run8(getattr(swa._lib, name), ptr=tuple(A + 4 if i == j else A for i in range(7))) == ARG
+
+
+def kv8(lib, ptr=(A,) * 8, W=64, B=2, Hq=8, Hkv=2, D=64, out=A, ws=A, nbytes=1 << 40, dtype=1):
+    return lib.swa_decode_kv8(*ptr, W, B, Hq, Hkv, D, out, ws, nbytes, dtype, None)
+
+
+def prefix(lib, ptr=(A,) * 8, N=5, W=64, B=2, Hq=8, Hkv=2, D=64, out=A, ws=A, nbytes=1 << 40, dtype=1):
+    return lib.swa_decode_prefix(*ptr[:5], N, *ptr[5:], W, B, Hq, Hkv, D, out, ws, nbytes, dtype, None)
+
+
+def sparse(lib, ptr=(A,) * 7, W=64, block=16, sel=4, first=1, last=1, B=2, Hq=8, Hkv=2, D=64, out=A, selected=A, ws=A,
+           nbytes=1 << 40, dtype=1):
+    return lib.swa_decode_sparse(*ptr, W, block, sel, first, last, B, Hq, Hkv, D, out, selected, ws, nbytes, dtype, None)
+
+
+COMMON = [
+    (dict(W=0), ARG), (dict(B=-1), ARG), (dict(Hq=0), ARG), (dict(Hkv=0), ARG), (dict(D=0), ARG), (dict(dtype=3), ARG),
+    (dict(Hq=7), SHAPE), (dict(Hq=18), UNSUPPORTED), (dict(D=32), UNSUPPORTED), (dict(D=96, dtype=0), UNSUPPORTED),
+    (dict(Hq=1 << 17, Hkv=1 << 17), SHAPE), (dict(B=1 << 25), SHAPE), (dict(out=None), ARG), (dict(out=A + 8), ARG),
+    (dict(ws=None), CAPACITY), (dict(nbytes=64), CAPACITY), (dict(ws=A + 8), ARG), (dict(B=0, out=None), 0),
+]
+
+
+@pytest.mark.parametrize("bad,status", COMMON)
+@pytest.mark.parametrize("step", [kv8, prefix, sparse])
+def test_step_refusals(swa, step, bad, status):
+    assert step(swa._lib, **bad) == status
+
+
+@pytest.mark.parametrize("step,n", [(kv8, 8), (prefix, 8), (sparse, 7)])
+def test_step_refuses_null_and_misaligned_pointers(swa, step, n):
+    for j in range(n):
+        assert step(swa._lib, ptr=tuple(None if i == j else A for i in range(n))) == ARG
+    for j in (0, 1, 2, 3, n - 1):
+        assert step(swa._lib, ptr=tuple(A + 4 if i == j else A for i in range(n))) == ARG
+
+
+def test_prefix_and_sparse_refusals(swa):
+    lib = swa._lib
+    assert prefix(lib, N=-1) == ARG
+    for bad, status in ((dict(block=48), UNSUPPORTED), (dict(block=0), UNSUPPORTED), (dict(sel=0), ARG),
+                        (dict(first=-1), ARG), (dict(last=-1), ARG), (dict(sel=1), SHAPE), (dict(sel=1 << 21), SHAPE),
+                        (dict(selected=None), ARG), (dict(selected=A + 2), ARG), (dict(B=40000), SHAPE)):
+        assert sparse(lib, **bad) == status, bad
+    bounds = lambda k=A, p=A, o=A, W=64, block=16, B=2, H=2, D=64, dt=1: lib.swa_block_bounds(k, p, o, W, block, B, H,  # noqa: E731
+                                                                                              D, dt, None)
+    assert bounds(B=0) == 0 and bounds(k=None) == ARG and bounds(p=None) == ARG and bounds(o=None) == ARG
+    assert bounds(W=0) == ARG and bounds(block=24) == UNSUPPORTED and bounds(D=32) == UNSUPPORTED
+    assert bounds(k=A + 8) == ARG and bounds(p=A + 4) == ARG and bounds(B=40000) == SHAPE
+
+
+def test_workspace_sizes(swa):
+    for fn, more in ((swa.swa_decode_kv8_workspace_bytes, ()), (swa.swa_decode_prefix_workspace_bytes, (700,)),
+                     (swa.swa_decode_sparse_workspace_bytes, (64,))):
+        n = fn(4, 8, 2, 64, 1000, *more)
+        assert n > 0 and fn(64, 8, 2, 64, 1000, *more) >= n
+        assert fn(0, 8, 2, 64, 1000, *more) == 0 and fn(4, 7, 2, 64, 1000, *more) == 0
+        assert fn(4, 8, 2, 48, 1000, *more) == 0 and fn(4, 8, 2, 64, 0, *more) == 0
+    assert swa.swa_decode_prefix_workspace_bytes(4, 8, 2, 64, 1000, -1) == 0
+    assert swa.swa_decode_sparse_workspace_bytes(4, 8, 2, 64, 1000, 20) == 0
+
+
+def test_binding_refuses_tensors_that_do_not_fit(swa):
+    bf, i64 = torch.bfloat16, torch.int64
+    q, kn, c = torch.zeros(2, 4, 64, dtype=bf), torch.zeros(2, 2, 64, dtype=bf), torch.zeros(2, 8, 2, 64, dtype=bf)
+    pos, out = torch.zeros(2, dtype=i64), torch.zeros(2, 4, 64, dtype=bf)
+    x8, e = torch.zeros(2, 8, 2, 64).to(torch.float8_e4m3fn), torch.zeros(2, 2, 8, dtype=torch.uint8)
+    pre = torch.zeros(5, 2, 64, dtype=bf)
+    for call in (
+        lambda: swa.swa_decode_kv8(q, kn, kn, x8, e, x8, e, pos, out),                    # not on a GPU
+        lambda: swa.swa_decode_kv8(q, kn, kn, c, e, c, e, pos, out),                      # not an 8-bit cache
+        lambda: swa.swa_decode_kv8(q, kn, kn, x8, e, x8, e, pos.int(), out),              # positions in 32 bits
+        lambda: swa.swa_decode_kv8(q, kn, kn, x8, e.transpose(1, 2), x8, e, pos, out),    # exponents [B, W, Hkv]
+        lambda: swa.swa_decode_prefix(q, kn, kn, pre, pre[:4], c, c, pos, out),           # prefix lengths differ
+        lambda: swa.swa_decode_prefix(q, kn.float(), kn, pre, pre, c, c, pos, out),       # types differ
+        lambda: swa.swa_decode_prefix(q[:1], kn[:1], kn[:1], pre, pre, c, c, pos[:1], out[:1]),  # batches differ
+        lambda: swa.swa_decode_sparse(q, kn, kn, c, c, torch.zeros(2, 2, 1, 2, 64, dtype=bf), pos, out,
+                                      torch.zeros(2, 1, 3, dtype=torch.int32), 16),       # selection of one head
+        lambda: swa.swa_block_bounds(c, pos, torch.zeros(2, 2, 2, 2, 64, dtype=bf), 8),   # bounds of more blocks
+        lambda: swa.swa_kv8_write(c, c, x8, e, x8, e, pos),                               # not on a GPU
+        lambda: swa.swa_kv8_read(x8, e, x8, e, pos, c, c.float()),                        # types differ
+        lambda: swa.swa_rope_nd(q, torch.zeros(2, 3, dtype=torch.int32), (12, 10, 10)),   # not on a GPU
+        lambda: swa.swa_rope_nd(q, torch.zeros(2, 2, dtype=torch.int32), (12, 10, 10)),   # axes differ
+    ):
+        with pytest.raises(ValueError):
+            call()
