@@ -153,6 +153,10 @@ cudaError_t launch_decode_tc(const DecodeParams& p, int sms, cudaStream_t stream
 cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t stream);
 // bf16 [B, N, H, D] as a 4-D map {D, H, N, B}, box 64 x 1 x 128 x 1, 128-byte swizzle
 bool encode_4d_sw128(CUtensorMap* m, const void* base, int D, int H, int64_t N, int B);
+// a tiled map of 1- or 2-byte (bf16) elements: sizes and box in elements, strides of all
+// but the innermost axis in bytes, swizzled over 64 or 128 bytes
+bool encode_tiled(CUtensorMap* m, int elem_bytes, const void* base, int rank, const uint64_t* dims,
+                  const uint64_t* strides, const uint32_t* box, int swizzle_bytes);
 int device_sms();
 // bf16 matrix [rows, inner] (inner contiguous) as a 2-D map; box = 64 columns x
 // box_rows rows, 128-byte swizzle

@@ -20,14 +20,15 @@ namespace swa {
 
 constexpr int kE8Min = -40, kE8Max = 40;
 
-// e of a row whose largest magnitude is a (a >= 0, not NaN; infinity counts as
-// larger than everything)
-SWA_DEV int kv8_exponent(float a) {
+// the least e with a <= 448 * 2^e, for a normal a > 0 (a smaller one: below -126; infinity: 120)
+SWA_DEV int exponent448(float a) {
   const uint32_t u = __float_as_uint(a);
   // a = 1.f * 2^(field - 127); 448 = 1.75 * 2^8
-  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return min(max(e, kE8Min), kE8Max);
+  return static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
 }
+
+// e of a cached row whose largest magnitude is a (not NaN)
+SWA_DEV int kv8_exponent(float a) { return min(max(exponent448(a), kE8Min), kE8Max); }
 
 // 2^e for e in the normal range
 SWA_DEV float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }

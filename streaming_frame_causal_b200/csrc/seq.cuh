@@ -24,6 +24,7 @@ namespace swa {
 constexpr int kSeqKeys = 128;     // keys of a tile
 constexpr int kSeqRows = 8;       // query heads of an item
 constexpr int kSeqMaxCtas = 512;  // CTAs that the workspace has partial slots for
+constexpr int kSeqCols = 16;      // query columns of the tensor-core products
 constexpr int kSeqMaxSplits = 64; // pieces of a shared prefix
 
 struct SeqParams {
@@ -47,6 +48,8 @@ struct SeqParams {
   float* part_ml;         // [slots, 8, 2] maximum in log2 units, sum
   float* pre_o;           // [splits, B * Hq, D]
   float* pre_ml;          // [splits, B * Hq, 2]
+  uint8_t* q8;            // 8-bit caches: [B * Hkv, 16, D] the queries as two e4m3 terms
+  float* q_scale;         // [B * Hq] 2^e of each
   int* err;
   int W, B, Hq, Hkv, G;   // G query heads per KV head
   int groups, items;      // groups of 8 heads per KV head; items per sequence = Hkv * groups
@@ -128,5 +131,13 @@ SWA_DEV int seq_slot(const SeqParams& p, int b, int kvh, int n_tokens, int t, in
   const int slot = blk * p.block + (i - j * p.block);
   return (blk >= 0 && slot < n_tokens) ? slot : -1;
 }
+
+// columns that G query heads take: 1, 2, 4 or 8
+SWA_HD int seq_head_columns(int G) { return G <= 2 ? G : (G <= 4 ? 4 : 8); }
+
+// the tensor-core kernel (seq_tc.cu), behind the preparation on the same stream: 16-bit
+// queries, head_dim 64 or 128, at most 8 query heads per KV head; p.ctas = seq_tc_ctas
+int seq_tc_ctas(int D, bool kv8, int sms);
+cudaError_t launch_seq_tc(const SeqParams& p, int D, bool kv8, cudaStream_t stream);
 
 }  // namespace swa

@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kPrepThreads) seq_prep_kernel(const __grid_con
     return;
   }
   constexpr int E = D / 32;  // elements of a lane
+  constexpr bool kSplitQ = KIND == SEQ_KV8 && sizeof(T) == 2;  // for the tensor cores (seq_tc.cu)
   const int64_t row = static_cast<int64_t>(blockIdx.x - 1) * kPrepWarps + warp;
   if (row >= static_cast<int64_t>(p.B) * p.Hkv) return;
   const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<int64_t>(b) * p.Hkv);
@@ -118,6 +119,41 @@ __global__ void __launch_bounds__(kPrepThreads) seq_prep_kernel(const __grid_con
       T* dst = static_cast<T*>(kv ? p.v_cache : p.k_cache) + at;
 #pragma unroll
       for (int i = 0; i < E; ++i) dst[i] = src[i];
+    }
+  }
+  if constexpr (kSplitQ) {
+    // query head g as hi in row g and lo in row columns + g of the item's 16 rows
+    const int cols = seq_head_columns(p.G);
+    uint8_t* dst = p.q8 + row * kSeqCols * D + lane * E;
+    for (int g = 0; g < kSeqCols; ++g) {
+      if (g < cols && g < p.G) {
+        const int64_t qrow = static_cast<int64_t>(b) * p.Hq + h * p.G + g;
+        const T* src = static_cast<const T*>(p.q) + qrow * D + lane * E;
+        float x[E], a = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          x[i] = to_f32(src[i]);
+          a = fmaxf(a, fabsf(x[i]));
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        const int e = min(max(exponent448(a), -118), 118);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const float y = x[i] * pow2i(-e);
+          const uint32_t hi = to_e4m3x2(y, 0.f);
+          dst[g * D + i] = static_cast<uint8_t>(hi);
+          dst[(cols + g) * D + i] = static_cast<uint8_t>(to_e4m3x2(y - from_e4m3x2(hi).x, 0.f));
+        }
+        // an infinite query has no softmax: its scores become NaN
+        if (lane == 0) p.q_scale[qrow] = a == INFINITY ? NAN : pow2i(e);
+      } else if (g < cols) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) dst[g * D + i] = dst[(cols + g) * D + i] = 0;
+      } else if (g >= 2 * cols) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) dst[g * D + i] = 0;
+      }
     }
   }
   if constexpr (KIND == SEQ_PLAIN) {
@@ -628,19 +664,19 @@ size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // The device buffers of a step inside the caller's workspace, in this order.
 struct SeqLayout {
-  size_t cum, share, part_o, part_ml, pre_o, pre_ml, score, bytes;
+  size_t cum, share, part_o, part_ml, pre_o, pre_ml, score, q8, q_scale, bytes;
 };
 
 // Pieces of the prefix for the CUDA-core kernel: enough for three CTAs per SM.
 int prefix_pieces(const SeqParams& p) {
-  if (p.N == 0) return 0;
+  if (p.N == 0 || p.B == 0) return 0;
   const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.Hkv;
   const int64_t want = (3 * 148 + ctas - 1) / ctas;
   const int tiles = cdiv(p.N, kSeqKeys);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, tiles, kSeqMaxSplits})));
 }
 
-SeqLayout seq_layout(const SeqParams& p, int D) {
+SeqLayout seq_layout(const SeqParams& p, int D, bool kv8) {
   SeqLayout l{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -657,6 +693,8 @@ SeqLayout seq_layout(const SeqParams& p, int D) {
   l.pre_o = take(pre * D * sizeof(float));
   l.pre_ml = take(pre * 2 * sizeof(float));
   l.score = take(p.block ? static_cast<size_t>(p.B) * p.Hkv * p.n_blocks * sizeof(uint64_t) : 0);
+  l.q8 = take(kv8 ? static_cast<size_t>(p.B) * p.Hkv * kSeqCols * D : 0);
+  l.q_scale = take(kv8 ? static_cast<size_t>(p.B) * p.Hq * sizeof(float) : 0);
   l.bytes = at;
   return l;
 }
@@ -672,7 +710,8 @@ swa_status seq_sizes(SeqParams& p, int D, int dtype) {
   p.groups = cdiv(p.G, kSeqRows);
   p.items = p.Hkv * p.groups;
   if (p.Hq > 65535 || static_cast<int64_t>(p.B) * p.Hq > (1ll << 26) ||
-      static_cast<int64_t>(p.B) * (p.W / kSeqKeys + 2) > 0x7fffffffll)
+      static_cast<int64_t>(p.B) * (p.W / kSeqKeys + 2) > 0x7fffffffll ||
+      static_cast<int64_t>(p.W) * p.Hkv * D > (1ll << 37))
     return SWA_ERR_SHAPE;
   p.splits = prefix_pieces(p);
   return SWA_OK;
@@ -690,7 +729,8 @@ cudaError_t allow_smem(K kernel, int bytes, DeviceOnce& once) {
 
 template <typename T, int D, int KIND>
 cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
-  p.ctas = std::min(3 * device_sms(), kSeqMaxCtas);
+  constexpr bool kTc = sizeof(T) == 2;  // 16-bit queries: the tensor cores
+  p.ctas = kTc ? seq_tc_ctas(D, KIND == SEQ_KV8, device_sms()) : std::min(3 * device_sms(), kSeqMaxCtas);
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv;
   seq_prep_kernel<T, D, KIND>
       <<<static_cast<unsigned>(1 + (rows + kPrepWarps - 1) / kPrepWarps), kPrepThreads, 0, st>>>(p);
@@ -713,7 +753,9 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
       ++launches;
     }
   }
-  if (e == cudaSuccess) {
+  if constexpr (kTc) {
+    if (e == cudaSuccess) e = launch_seq_tc(p, D, KIND == SEQ_KV8, st);
+  } else if (e == cudaSuccess) {
     static DeviceOnce once;
     e = allow_smem(seq_simt_kernel<T, D, KIND>, SimtPlan<D>::kSmem, once);
     if (e == cudaSuccess)
@@ -745,7 +787,7 @@ swa_status seq_step(SeqParams& p, int D, int dtype, void* workspace, size_t work
       !al16(p.k_prefix) || !al16(p.v_prefix) || !al16(p.bounds) || (reinterpret_cast<uintptr_t>(p.pos) & 7u) ||
       (reinterpret_cast<uintptr_t>(p.selected) & 3u))
     return SWA_ERR_ARG;
-  const SeqLayout l = seq_layout(p, D);
+  const SeqLayout l = seq_layout(p, D, KIND == SEQ_KV8);
   if (!workspace || workspace_bytes < l.bytes) return SWA_ERR_CAPACITY;
   if (!al16(workspace)) return SWA_ERR_ARG;
   if (const int ds = device_ready_status(&p.err)) return static_cast<swa_status>(ds);
@@ -757,6 +799,8 @@ swa_status seq_step(SeqParams& p, int D, int dtype, void* workspace, size_t work
   p.pre_o = reinterpret_cast<float*>(ws + l.pre_o);
   p.pre_ml = reinterpret_cast<float*>(ws + l.pre_ml);
   p.score = reinterpret_cast<uint64_t*>(ws + l.score);
+  p.q8 = ws + l.q8;
+  p.q_scale = reinterpret_cast<float*>(ws + l.q_scale);
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
   return launch_step_d<KIND>(p, D, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
@@ -781,9 +825,9 @@ SeqParams seq_params(const void* q, const void* k_new, const void* v_new, void* 
 bool block_size(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
 
 // the workspace of a step of these sizes: enough for either type
-size_t workspace_of(SeqParams p, int D) {
+size_t workspace_of(SeqParams p, int D, bool kv8) {
   if (p.B < 1 || seq_sizes(p, D, SWA_F32) != SWA_OK) return 0;
-  return seq_layout(p, D).bytes;
+  return seq_layout(p, D, kv8).bytes;
 }
 
 }  // namespace
@@ -792,13 +836,14 @@ size_t workspace_of(SeqParams p, int D) {
 using namespace swa;
 
 extern "C" size_t swa_decode_kv8_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W) {
-  return workspace_of(seq_params(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W, B, Hq, Hkv, nullptr), head_dim);
+  return workspace_of(seq_params(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W, B, Hq, Hkv, nullptr), head_dim,
+                      true);
 }
 
 extern "C" size_t swa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W, int N) {
   SeqParams p = seq_params(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W, B, Hq, Hkv, nullptr);
   p.N = N;
-  return workspace_of(p, head_dim);
+  return workspace_of(p, head_dim, false);
 }
 
 extern "C" size_t swa_decode_sparse_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int W, int block) {
@@ -806,7 +851,7 @@ extern "C" size_t swa_decode_sparse_workspace_bytes(int B, int Hq, int Hkv, int 
   SeqParams p = seq_params(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, W, B, Hq, Hkv, nullptr);
   p.block = block;
   p.n_blocks = cdiv(W, block);
-  return workspace_of(p, head_dim);
+  return workspace_of(p, head_dim, false);
 }
 
 extern "C" swa_status swa_decode_kv8(const void* q, const void* k_new, const void* v_new, void* k8, uint8_t* k_exp,

@@ -1,0 +1,652 @@
+// seq_tc.cu -- the attention of the per-sequence decode steps on the tensor cores
+// (sm_100a): 16-bit queries against a 16-bit cache (all of it, or selected blocks)
+// or the 8-bit cache, head_dim 64 or 128, up to 8 query heads per KV head.
+//
+// One new token gives only G <= 8 query rows per (sequence, KV head), so the products
+// run with the keys (then the output elements) as the M dimension:
+//   S^T[128 keys x 16]  = K_tile[128 x D] . Q^T      (A = K, K-major;  B = Q, K-major)
+//   O^T[128 x 16 or 32] += V_tile^T . P^T            (A = V, MN-major; B = P^T, K-major)
+// S^T has one key per tensor-memory lane and softmax thread.  The reference
+// maximum of a head moves only when a tile exceeds it by 2^kGrow; the output
+// accumulators are then rescaled in place.
+//
+// The 8-bit cache is multiplied as it is stored (kind::f8f6f4), with no
+// conversion of the 2 D bytes a key brings.  The 16-bit operands on the other
+// side are split instead, into columns that the products have to spare:
+//   Q    q 2^-e = hi + lo, both e4m3: 4 + 4 significant bits hold a bf16 value exactly
+//        down to 2^-9, e the row's exponent, so an element is off by 2^-10 at most where
+//        the largest is above 224 (2^-18 of it).  S = (S_hi + S_lo) 2^(e_q + e_k).
+//   P    the weight of key i on V is p_i 2^(e_v,i), which reaches over many binades and
+//        gets the wide type: w 2^11 = a + b + c, each e5m2 (3 significant bits, down to
+//        2^-16).  A 16-bit float cut after its top byte is an e5m2, so a and b are the
+//        top bytes of what is left and c is rounded: 9 significant bits in all, as bf16
+//        has 8, down to 2^-28 of the largest weight.  The softmax reference is
+//        taken over log2 p + e_v so that w stays in range, and the row sum adds
+//        w 2^(-e_v).
+// The three products' columns are added when the item is finished.
+//
+// CTA (192 threads): warp 0 producer (TMA: K and V tiles through a ring across the
+// items of the CTA's share, Q double-buffered), warp 1 TMEM allocator and MMA issuer
+// (the whole warp runs the loop, one elected lane issues), warps 2-5 softmax.  S^T
+// and P^T are double-buffered, and S^T of tile j + 1 is issued before O^T of tile j.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "kv8.cuh"
+#include "ptx.cuh"
+#include "seq.cuh"
+
+namespace swa {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kN = kSeqCols;  // columns of S^T
+
+template <int D, int GP, bool KV8>
+struct SeqTcPlan {
+  static constexpr int kElem = KV8 ? 1 : 2;
+  static constexpr int kRowBytes = D * kElem;                         // a row of K or V
+  static constexpr int kSubBytesRow = kRowBytes < 128 ? kRowBytes : 128;  // of a swizzled sub-tile
+  static constexpr int kSubs = kRowBytes / kSubBytesRow;
+  static constexpr int kSub = kSeqKeys * kSubBytesRow;
+  static constexpr int kTile = kSubs * kSub;
+  static constexpr int kStage = 2 * kTile;
+  // CTAs per SM: the softmax of a tile is a chain of latencies (TMEM load, exchange
+  // between the warps, hand-off), which two CTAs overlap where 96 KB of ring are deep
+  // enough; a 16-bit tile at head_dim 128 fills 64 KB, and the SM's memory takes one CTA
+  static constexpr int kPerSm = kStage <= 32 * 1024 ? 2 : 1;
+  static constexpr int kStages = (kPerSm == 2 ? 96 : 192) * 1024 / kStage;
+  static constexpr int kON = KV8 && GP == 8 ? 32 : 16;                // columns of O^T
+  static constexpr int kQSub = kN * kSubBytesRow;
+  static constexpr int kQ = kSubs * kQSub;
+  static constexpr int kPSub = kN * 128;
+  static constexpr int kP = KV8 ? kON * 128 : 2 * kPSub;  // rows of 128 bytes; 16-bit: of two 128-byte halves
+  // a stage holds V, then K: at head_dim 64 the second product reads 64 rows of M past
+  // its V tile (rows D..127 of O^T, never read), which is then the K tile beside it
+  static constexpr int kOffK = kTile;
+  static constexpr int kOffQ = kStages * kStage;
+  static constexpr int kOffP = kOffQ + 2 * kQ;
+  static constexpr int kOffRed = kOffP + 2 * kP;  // [2][4][8] tile maxima, [4][8] row sums
+  static constexpr int kOffBar = kOffRed + 3 * 4 * kSeqRows * 4;
+  static constexpr int kNumBars = 2 + 2 + 2 * kStages + 2 + 2 + 2 + 4;
+  static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+  static constexpr int kSmem = kOffTmem + 16 + 1024;  // + alignment slack
+  static_assert((kSmem + 1024) * kPerSm <= 228 * 1024, "shared memory");
+  static_assert(kQ % 1024 == 0 && kP % 1024 == 0, "swizzle atoms");
+  static constexpr uint32_t kTmemCols = 64;  // S^T 2 x 16 | O^T 16 or 32
+  static constexpr float kGrow = KV8 ? 4.f : 8.f;
+};
+
+constexpr float kPScale = 2048.f;  // 2^11: weights up to 2^(11 + 4) fit e5m2's 57344
+
+struct SeqTcParams {
+  SeqParams s;
+  CUtensorMap tm_k, tm_v;  // [B, W, Hkv, D], box 128 rows (or a block's) of one head
+  CUtensorMap tm_q;        // bf16 [B * Hq, D], or the split queries [B * Hkv * 16, D]
+};
+
+SWA_DEV void tma_2d(uint32_t dst, const void* tmap, uint32_t mbar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(mbar)
+      : "memory");
+}
+
+SWA_DEV void st_b16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+SWA_DEV void st_b8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+SWA_DEV void st_zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+
+// maximum over the warp (NaN passed over)
+SWA_DEV float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
+// kind::f8f6f4 counterpart of mma_ss_if
+SWA_DEV void mma8_ss_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
+}
+
+// kind::f8f6f4 instruction descriptor: A e4m3, B e4m3 (0) or e5m2 (1), 32-bit sums
+constexpr uint32_t idesc_f8(int n, uint32_t b_type, uint32_t a_mn_major) {
+  return (1u << 4) | (b_type << 10) | (a_mn_major << 15) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// descriptor of a tile whose rows are 128 or 64 bytes, swizzled to their width
+template <int RowBytes>
+SWA_DEV uint64_t sdesc_rows(uint32_t addr, uint32_t lbo) {
+  uint64_t d = sdesc_sw128(addr, lbo, 8 * RowBytes);
+  if (RowBytes == 64) d ^= static_cast<uint64_t>(2 ^ 4) << 61;  // 64-byte swizzle
+  return d;
+}
+
+// e4m3 and e5m2 hold what the comments above say; a and b are the top bytes of v
+// and of what they leave, c the rounded rest (two values at a time)
+SWA_DEV void split_e5m2(float x0, float x1, uint32_t* t) {
+  __half2 v = __floats2half2_rn(x0, x1);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    t[i] = *reinterpret_cast<uint32_t*>(&v) & 0xff00ff00u;
+    v = __hsub2(v, *reinterpret_cast<__half2*>(&t[i]));
+  }
+  // what is left is below 2^10, so the carry of the rounding stays in its half
+  t[2] = *reinterpret_cast<uint32_t*>(&v) + 0x00800080u;
+}
+
+template <int D, int GP, bool KV8>
+__global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
+    seq_tc_kernel(const __grid_constant__ SeqTcParams tp) {
+  using PL = SeqTcPlan<D, GP, KV8>;
+  constexpr int kStages = PL::kStages;
+  const SeqParams& p = tp.s;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t base = (raw_base + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw_base);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  griddep_launch_dependents();
+
+  const uint32_t bar0 = base + PL::kOffBar;
+  auto q_full = [&](int i) { return bar0 + 8u * i; };
+  auto q_free = [&](int i) { return bar0 + 8u * (2 + i); };
+  auto kv_full = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (4 + kStages + s); };
+  constexpr int kB = 4 + 2 * kStages;
+  auto s_full = [&](int i) { return bar0 + 8u * (kB + i); };
+  auto p_full = [&](int i) { return bar0 + 8u * (kB + 2 + i); };
+  auto p_free = [&](int i) { return bar0 + 8u * (kB + 4 + i); };
+  const uint32_t o_done = bar0 + 8u * (kB + 6);  // every second product complete
+  const uint32_t o_full = bar0 + 8u * (kB + 7);  // an item's last second product complete
+  const uint32_t drain = bar0 + 8u * (kB + 8);
+  const uint32_t xbar = bar0 + 8u * (kB + 9);    // the 128 softmax threads
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full(i), 1);
+      mbar_init(q_free(i), 1);
+      mbar_init(s_full(i), 1);
+      mbar_init(p_full(i), 128);
+      mbar_init(p_free(i), 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 1);
+    }
+    mbar_init(o_done, 1);
+    mbar_init(o_full, 1);
+    mbar_init(drain, 1);
+    mbar_init(xbar, 128);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(base + PL::kOffTmem, PL::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + PL::kOffTmem);
+  griddep_wait();  // the division of the work, the new token, the selection
+
+  SeqWalk walk;
+  walk.start(p, blockIdx.x);
+  SeqRun run;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    // the lanes issue the boxes of a tile side by side: one box of 128 rows per sub-tile
+    // of K and of V, or one per selected block (8 of them at most, 32 pieces)
+    if (lane == 0) {
+      tma_prefetch_desc(&tp.tm_k);
+      tma_prefetch_desc(&tp.tm_v);
+      tma_prefetch_desc(&tp.tm_q);
+    }
+    const int rows = p.block ? p.block : kSeqKeys;  // of a box
+    const int per_tile = kSeqKeys / rows;
+    int lu = 0, jj = 0;
+    bool ok = true;
+    while (ok && walk.next(p, blockIdx.x, run)) {
+      const int qb = lu & 1;
+      if (lu >= 2 &&
+          !__all_sync(0xffffffffu, mbar_wait(q_free(qb), ((lu >> 1) - 1) & 1, p.err, ERR_WAIT_TMA))) {
+        ok = false;
+        break;
+      }
+      const int kvh = run.item;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full(qb), PL::kQ);
+        for (int sub = 0; sub < PL::kSubs; ++sub)
+          tma_2d(base + PL::kOffQ + qb * PL::kQ + sub * PL::kQSub, &tp.tm_q, q_full(qb), sub * 64,
+                 KV8 ? (run.b * p.Hkv + kvh) * kN : run.b * p.Hq + kvh * p.G);
+      }
+      ++lu;
+      const int* sel = p.block ? p.selected + (static_cast<int64_t>(run.b) * p.Hkv + kvh) * p.n_select : nullptr;
+      const int n_blocks = p.block ? min((seq_tokens(p, run.b) + p.block - 1) / p.block, p.n_select) : 0;
+      for (int j = 0; j < run.tiles; ++j, ++jj) {
+        const int st = jj % kStages;
+        const int first = (run.t0 + j) * per_tile;  // box of the item
+        const int boxes = p.block ? min(per_tile, n_blocks - first) : 1;
+        // this lane's piece: of box lane / (2 kSubs), K or V, sub-tile
+        const int box = lane / (2 * PL::kSubs), piece = lane % (2 * PL::kSubs);
+        const int kv = piece / PL::kSubs, sub = piece % PL::kSubs;
+        const int row = box >= boxes ? -1 : (p.block ? sel[first + box] * p.block : first * kSeqKeys);
+        if (jj >= kStages && !__all_sync(0xffffffffu, mbar_wait(kv_empty(st), ((jj / kStages) - 1) & 1, p.err,
+                                                                 ERR_WAIT_TMA))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(kv_full(st), 2 * boxes * rows * PL::kRowBytes);
+        __syncwarp();
+        if (row >= 0)
+          tma_load_4d(base + st * PL::kStage + (kv ? 0 : PL::kOffK) + sub * PL::kSub + box * rows * PL::kSubBytesRow,
+                      kv ? &tp.tm_v : &tp.tm_k, kv_full(st), sub * 64, kvh, row, run.b);
+      }
+    }
+    // never leave with a bulk copy still landing in shared memory
+    for (int j = jj - kStages; j < jj; ++j)
+      if (j >= 0) mbar_wait(kv_full(j % kStages), (j / kStages) & 1, p.err, ERR_WAIT_TMA);
+    for (int i = lu - 2; i < lu; ++i)
+      if (i >= 0) mbar_wait(q_full(i & 1), (i >> 1) & 1, p.err, ERR_WAIT_TMA);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t issue = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, ERR_WAIT_MMA));
+    };
+    const uint64_t dk0 = sdesc_rows<PL::kSubBytesRow>(base + PL::kOffK, 16);  // K of stage 0 (A, K-major)
+    // V of stage 0 (A, MN-major): groups of M rows are sub-tiles apart
+    const uint64_t dv0 = sdesc_rows<PL::kSubBytesRow>(base, PL::kSub);
+    const uint64_t dq0 = sdesc_rows<PL::kSubBytesRow>(base + PL::kOffQ, 16);  // (B, K-major)
+    const uint64_t dp0 = sdesc_rows<128>(base + PL::kOffP, 16);               // (B, K-major)
+    auto issue_s = [&](int jj, int qb) {
+      const uint64_t dk = dk0 + (jj % kStages) * static_cast<uint64_t>(PL::kStage >> 4);
+      const uint64_t dq = dq0 + qb * static_cast<uint64_t>(PL::kQ >> 4);
+      const uint32_t tS = tm + (jj & 1) * kN;
+#pragma unroll
+      for (int kk = 0; kk < PL::kRowBytes / 32; ++kk) {  // 32 bytes of D an instruction
+        const uint64_t a = dk + (((kk >> 2) * PL::kSub + (kk & 3) * 32) >> 4);
+        const uint64_t b = dq + (((kk >> 2) * PL::kQSub + (kk & 3) * 32) >> 4);
+        if constexpr (KV8)
+          mma8_ss_if(issue, tS, a, b, idesc_f8(kN, 0, 0), kk > 0 ? 1u : 0u);
+        else
+          mma_ss_if(issue, tS, a, b, idesc_bf16_f32(128, kN, 0), kk > 0 ? 1u : 0u);
+      }
+    };
+    auto issue_o = [&](int jj, bool acc) {
+      const uint64_t dv = dv0 + (jj % kStages) * static_cast<uint64_t>(PL::kStage >> 4);
+      const uint64_t dp = dp0 + (jj & 1) * static_cast<uint64_t>(PL::kP >> 4);
+      const uint32_t tO = tm + 2 * kN;
+      constexpr int kKeys = 32 / PL::kElem;  // keys of an instruction
+#pragma unroll
+      for (int kk = 0; kk < kSeqKeys / kKeys; ++kk) {
+        const uint64_t a = dv + ((kk * kKeys * PL::kSubBytesRow) >> 4);
+        const uint64_t b = dp + (((kk >> 2) * PL::kPSub + (kk & 3) * 32) >> 4);
+        if constexpr (KV8)
+          mma8_ss_if(issue, tO, a, b, idesc_f8(PL::kON, 1, 1), (acc || kk > 0) ? 1u : 0u);
+        else
+          mma_ss_if(issue, tO, a, b, idesc_bf16_f32(128, kN, 0) | (1u << 15), (acc || kk > 0) ? 1u : 0u);
+      }
+    };
+    int lu = 0, jj = 0;
+    int prev = -1;  // tile whose second product is pending
+    bool prev_first = false, prev_last = false, ok = true;
+    auto finish_prev = [&]() -> bool {
+      if (!wait(p_full(prev & 1), (prev >> 1) & 1)) return false;
+      tc_fence_after();
+      issue_o(prev, !prev_first);
+      mma_commit_if(issue, kv_empty(prev % kStages));
+      mma_commit_if(issue, p_free(prev & 1));
+      mma_commit_if(issue, o_done);
+      if (prev_last) mma_commit_if(issue, o_full);
+      return true;
+    };
+    while (ok && walk.next(p, blockIdx.x, run)) {
+      const int qb = lu & 1;
+      if (!wait(q_full(qb), (lu >> 1) & 1)) {
+        ok = false;
+        break;
+      }
+      ++lu;
+      for (int j = 0; j < run.tiles; ++j, ++jj) {
+        if (!wait(kv_full(jj % kStages), (jj / kStages) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_s(jj, qb);
+        mma_commit_if(issue, s_full(jj & 1));
+        if (j == run.tiles - 1) mma_commit_if(issue, q_free(qb));
+        if (prev >= 0 && !finish_prev()) {
+          ok = false;
+          break;
+        }
+        prev = jj;
+        prev_first = (j == 0);
+        prev_last = (j == run.tiles - 1);
+      }
+    }
+    if (ok && prev >= 0) finish_prev();
+    if (jj > 0) {
+      mma_commit_if(issue, drain);
+      wait(drain, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int quarter = warp & 3;          // TMEM lane quarter
+    const int r = quarter * 32 + lane;     // key within a tile; output element in O^T
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tO = tmem + lane_off + 2 * kN;
+    float* red = reinterpret_cast<float*>(gbase + PL::kOffRed);  // [2][4][8] maxima, then [4][8] sums
+    int jj = 0, nu = 0, nx = 0;  // tiles, finished items, exchanges so far
+    bool ok = true;
+    auto exchange = [&]() -> bool {
+      mbar_arrive(xbar);
+      return __all_sync(0xffffffffu, mbar_wait(xbar, (nx++) & 1, p.err, ERR_WAIT_SOFTMAX));
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, ERR_WAIT_SOFTMAX));
+    };
+    while (ok && walk.next(p, blockIdx.x, run)) {
+      const int kvh = run.item, b = run.b;
+      const int64_t qrow = static_cast<int64_t>(b) * p.Hq + kvh * p.G;
+      const int n_tokens = seq_tokens(p, b);
+      const int64_t ebase = (static_cast<int64_t>(b) * p.Hkv + kvh) * p.W;
+      float m[GP], l[GP], c[GP];
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+        c[h] = p.scale_log2;
+        if constexpr (KV8) c[h] *= h < p.G ? p.q_scale[qrow + h] : 0.f;
+      }
+      // this key's place and exponents, a tile ahead of their use
+      int slot = seq_slot(p, b, kvh, n_tokens, run.t0, r), ke = 127, ve = 127;
+      if (KV8 && slot >= 0) {
+        ke = p.k_exp[ebase + slot];
+        ve = p.v_exp[ebase + slot];
+      }
+      for (int j = 0; j < run.tiles; ++j, ++jj) {
+        const int sb = jj & 1;
+        const bool valid = slot >= 0;
+        const int ke0 = ke, ve0 = ve;
+        if (j + 1 < run.tiles) {
+          slot = seq_slot(p, b, kvh, n_tokens, run.t0 + j + 1, r);
+          if (KV8) {
+            ke = ve = 127;
+            if (slot >= 0) {
+              ke = p.k_exp[ebase + slot];
+              ve = p.v_exp[ebase + slot];
+            }
+          }
+        }
+        if (!wait(s_full(sb), (jj >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sv[16];
+        tmem_ld16(tmem + lane_off + sb * kN, sv);
+        tmem_wait_ld();
+        if (!valid) {
+          // The key's V row in the tile is whatever the slot or the stage held.  Its weight
+          // is 0, but 0 x NaN is NaN, so the row is zeroed before the second product
+          // reads it (the proxy fence before the p_full arrival orders these stores first).
+          const uint32_t vrow = base + (jj % kStages) * PL::kStage + r * PL::kSubBytesRow;
+#pragma unroll
+          for (int sub = 0; sub < PL::kSubs; ++sub)
+#pragma unroll
+            for (int o = 0; o < PL::kSubBytesRow; o += 16) st_zero16(vrow + sub * PL::kSub + o);
+        }
+        float x[GP];
+        const float kscale = KV8 ? __uint_as_float(static_cast<uint32_t>(ke0) << 23) : 1.f;
+        const float vexp = static_cast<float>(ve0 - 127);
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          float s = __uint_as_float(sv[h]);
+          if constexpr (KV8) s = fmaf((s + __uint_as_float(sv[GP + h])) * kscale, c[h], vexp);
+          else s *= c[h];
+          x[h] = valid ? s : -INFINITY;
+        }
+        // tile maximum per head: over the warp, then over the four warps
+        float* rb = red + sb * 4 * kSeqRows;
+#pragma unroll
+        for (int h = 0; h < GP; ++h) {
+          const float v = warp_max(x[h]);
+          if (lane == 0) rb[quarter * kSeqRows + h] = v;
+        }
+        if (!exchange()) {
+          ok = false;
+          break;
+        }
+        float top[GP];
+#pragma unroll
+        for (int h = 0; h < GP; ++h)
+          top[h] = fmaxf(fmaxf(rb[h], rb[kSeqRows + h]), fmaxf(rb[2 * kSeqRows + h], rb[3 * kSeqRows + h]));
+        // P^T buffer sb is free once the second product of tile jj-2 has completed
+        if (jj >= 2 && !wait(p_free(sb), ((jj >> 1) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        if (j == 0) {
+#pragma unroll
+          for (int h = 0; h < GP; ++h) m[h] = top[h];
+        } else {
+          bool grow = false;
+#pragma unroll
+          for (int h = 0; h < GP; ++h) grow |= top[h] > m[h] + PL::kGrow;
+          if (grow) {
+            // O^T holds tiles up to jj-1 of this item: wait for the last of them, then
+            // rescale the heads whose reference maximum moves
+            if (!wait(o_done, (jj - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            float alpha[GP];
+#pragma unroll
+            for (int h = 0; h < GP; ++h) {
+              alpha[h] = 1.f;
+              if (top[h] > m[h] + PL::kGrow) {
+                alpha[h] = ex2_approx(m[h] - top[h]);
+                l[h] *= alpha[h];
+                m[h] = top[h];
+              }
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < PL::kON; c0 += 16) {
+              uint32_t ov[16];
+              tmem_ld16(tO + c0, ov);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (c0 + i < (KV8 ? 3 : 1) * GP)
+                  ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha[(c0 + i) % GP]);
+              tmem_st16(tO + c0, ov);
+            }
+            tmem_wait_st();
+          }
+        }
+        const uint32_t pb = base + PL::kOffP + sb * PL::kP;
+        if constexpr (KV8) {
+          // P^T rows (term, head) of 128 bytes, the 128-byte-swizzled K-major layout
+          const float sum_scale = __uint_as_float(static_cast<uint32_t>(254 - ve0) << 23);  // 2^-e_v
+          const uint32_t col = r & 15;
+          auto put = [&](int row, uint32_t v) {
+            st_b8(pb + row * 128 + (((r >> 4) ^ (row & 7)) << 4) + col, v);
+          };
+#pragma unroll
+          for (int h = 0; h < GP; h += 2) {
+            const float e0 = ex2_approx(x[h] - m[h]);
+            const float e1 = h + 1 < GP ? ex2_approx(x[h + 1 < GP ? h + 1 : h] - m[h + 1 < GP ? h + 1 : h]) : 0.f;
+            l[h] = fmaf(e0, sum_scale, l[h]);
+            if (h + 1 < GP) l[h + 1 < GP ? h + 1 : h] = fmaf(e1, sum_scale, l[h + 1 < GP ? h + 1 : h]);
+            uint32_t t[3];
+            split_e5m2(e0 * kPScale, e1 * kPScale, t);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              put(i * GP + h, t[i] >> 8);
+              if (h + 1 < GP) put(i * GP + h + 1, t[i] >> 24);
+            }
+          }
+        } else {
+          // P^T[h][key] in the 128-byte-swizzled K-major layout (row h, 64-key sub-tiles)
+          const uint32_t ph = pb + (r >> 6) * PL::kPSub;
+          const int col = r & 63;
+#pragma unroll
+          for (int h = 0; h < GP; ++h) {
+            const float pe = ex2_approx(x[h] - m[h]);
+            l[h] += pe;
+            const __nv_bfloat16 bv = __float2bfloat16_rn(pe);
+            st_b16(ph + h * 128 + ((((col >> 3) ^ (h & 7))) << 4) + (col & 7) * 2,
+                   *reinterpret_cast<const uint16_t*>(&bv));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full(sb));
+      }
+      if (!ok) break;
+      // ---- the item's result: sums over the threads' keys, O^T row by row
+      float* lsum = red + 2 * 4 * kSeqRows;
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        float v = l[h];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if (lane == 0) lsum[quarter * kSeqRows + h] = v;
+      }
+      if (!exchange()) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int h = 0; h < GP; ++h)
+        l[h] = (lsum[h] + lsum[kSeqRows + h]) + (lsum[2 * kSeqRows + h] + lsum[3 * kSeqRows + h]);
+      if (!wait(o_full, nu & 1)) {
+        ok = false;
+        break;
+      }
+      ++nu;
+      tc_fence_after();
+      uint32_t ov[PL::kON];
+#pragma unroll
+      for (int c0 = 0; c0 < PL::kON; c0 += 16) tmem_ld16(tO + c0, ov + c0);
+      tmem_wait_ld();
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        float o = __uint_as_float(ov[h]);
+        if constexpr (KV8)
+          o = (o + (__uint_as_float(ov[GP + h]) + __uint_as_float(ov[2 * GP + h]))) * (1.f / kPScale);
+        if (r < D && h < p.G) {
+          if (run.slot < 0) {
+            static_cast<__nv_bfloat16*>(p.out)[(qrow + h) * D + r] = __float2bfloat16_rn(o / l[h]);
+          } else {
+            const int64_t at = static_cast<int64_t>(run.slot) * kSeqRows + h;
+            p.part_o[at * D + r] = o;
+            if (r == 0) {
+              p.part_ml[at * 2] = m[h];
+              p.part_ml[at * 2 + 1] = l[h];
+            }
+          }
+        }
+      }
+      // the sums are rewritten only after the next item's first exchange, which every
+      // thread reaches after reading them here
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, PL::kTmemCols);
+  }
+}
+
+template <int D, int GP, bool KV8>
+cudaError_t launch_g(const SeqTcParams& p, cudaStream_t st) {
+  using PL = SeqTcPlan<D, GP, KV8>;
+  static DeviceOnce attr_set;  // devices on which the smem opt-in was set
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  if (!attr_set.done(dev)) {
+    const cudaError_t e = cudaFuncSetAttribute(seq_tc_kernel<D, GP, KV8>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, PL::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set.mark(dev);
+  }
+  count_launches(1);
+  return launch_after(seq_tc_kernel<D, GP, KV8>, dim3(p.s.ctas), dim3(kThreads), PL::kSmem, st, p);
+}
+
+template <int D, bool KV8>
+cudaError_t launch_d(const SeqTcParams& p, cudaStream_t st) {
+  // built for 1, 2, 4 and 8 query heads; a group between them leaves columns unread
+  switch (seq_head_columns(p.s.G)) {
+    case 1: return launch_g<D, 1, KV8>(p, st);
+    case 2: return launch_g<D, 2, KV8>(p, st);
+    case 4: return launch_g<D, 4, KV8>(p, st);
+    default: return launch_g<D, 8, KV8>(p, st);
+  }
+}
+
+}  // namespace
+
+int seq_tc_ctas(int D, bool kv8, int sms) {
+  const bool two = kv8 || D == 64;
+  static_assert(SeqTcPlan<128, 8, true>::kPerSm == 2 && SeqTcPlan<64, 8, true>::kPerSm == 2 &&
+                    SeqTcPlan<64, 8, false>::kPerSm == 2 && SeqTcPlan<128, 8, false>::kPerSm == 1,
+                "CTAs per SM");
+  return std::min(two ? 2 * sms : sms, kSeqMaxCtas);
+}
+
+cudaError_t launch_seq_tc(const SeqParams& s, int D, bool kv8, cudaStream_t st) {
+  SeqTcParams p{};
+  p.s = s;
+  const uint64_t e = kv8 ? 1 : 2;
+  const uint32_t cols = static_cast<uint32_t>(std::min<uint64_t>(D, 128 / e));  // of a sub-tile
+  const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(s.Hkv), static_cast<uint64_t>(s.W),
+                            static_cast<uint64_t>(s.B)};
+  const uint64_t row = s.Hkv * D * e;
+  const uint64_t strides[3] = {D * e, row, row * s.W};
+  const uint32_t box[4] = {cols, 1, static_cast<uint32_t>(s.block ? s.block : kSeqKeys), 1};
+  const uint64_t qdims[2] = {static_cast<uint64_t>(D),
+                             kv8 ? static_cast<uint64_t>(s.B) * s.Hkv * kN : static_cast<uint64_t>(s.B) * s.Hq};
+  const uint64_t qstride[1] = {D * e};
+  const uint32_t qbox[2] = {cols, kN};
+  const int swizzle = static_cast<int>(cols * e);
+  if (!encode_tiled(&p.tm_k, static_cast<int>(e), s.k_cache, 4, dims, strides, box, swizzle) ||
+      !encode_tiled(&p.tm_v, static_cast<int>(e), s.v_cache, 4, dims, strides, box, swizzle) ||
+      !encode_tiled(&p.tm_q, static_cast<int>(e), kv8 ? s.q8 : s.q, 2, qdims, qstride, qbox, swizzle))
+    return cudaErrorInvalidValue;
+  if (kv8) return D == 64 ? launch_d<64, true>(p, st) : launch_d<128, true>(p, st);
+  return D == 64 ? launch_d<64, false>(p, st) : launch_d<128, false>(p, st);
+}
+
+}  // namespace swa
