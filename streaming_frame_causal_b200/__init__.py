@@ -317,14 +317,24 @@ def swa_decode_noalloc(q, k_new, v_new, k_cache, v_cache, pos: int, out, stream=
 def _cuda(*tensors) -> torch.device:
     """The CUDA device that all the tensors are on."""
     dev = tensors[0].device
-    if dev.type != "cuda" or any(t.device != dev for t in tensors):
-        raise ValueError(f"tensors must be on one CUDA device, got {[str(t.device) for t in tensors]}")
+    for t in tensors:
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"tensors must be on one CUDA device, got {[str(t.device) for t in tensors]}")
     return dev
 
 
 def _like(what: str, t, shape, dtype) -> None:
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what}: want {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _on(dev: torch.device, stream, call):
+    """call(stream handle) with ``dev`` current; the handle is the device's current
+    stream where ``stream`` is None."""
+    if dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
 
 
 def _token_rows(what: str, t) -> tuple[int, int]:
@@ -352,14 +362,13 @@ def swa_rope_nd(x, pos, pairs, theta: float = 10000.0, inverse: bool = False, ou
     is the call with ``inverse=True`` on the output's gradient (see include/swa.h)."""
     out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
     dev = _cuda(x, pos, out)
-    _like("pos", pos, tuple(x.shape[:-2]) + (len(pairs),), torch.int32)
+    _like("pos", pos, x.shape[:-2] + (len(pairs),), torch.int32)
     _like("out", out, x.shape, x.dtype)
     H, D = x.shape[-2:]
     (n, xs), (_, ys) = _token_rows("x", x), _token_rows("out", out)
-    with torch.cuda.device(dev):
-        _check(_lib.swa_rope_nd(x.data_ptr(), out.data_ptr(), _ptr(pos), n, H, D, xs, ys, len(pairs),
-                                (C.c_int32 * max(1, len(pairs)))(*pairs), float(theta), int(bool(inverse)),
-                                _dtype_code(x), _stream(stream)), "swa_rope_nd")
+    _check(_on(dev, stream, lambda st: _lib.swa_rope_nd(
+        x.data_ptr(), out.data_ptr(), _ptr(pos), n, H, D, xs, ys, len(pairs),
+        (C.c_int32 * max(1, len(pairs)))(*pairs), float(theta), int(bool(inverse)), _dtype_code(x), st)), "swa_rope_nd")
     return out
 
 
@@ -385,9 +394,8 @@ def _run8(fn, name, k, v, k8, k_exp, v8, v_exp, pos, count, stream, write):
     cache = [_ptr(k8), _ptr(k_exp), _ptr(v8), _ptr(v_exp)]
     run = [_ptr(k), _ptr(v)]
     at = [_ptr(pos), _ptr(count)]
-    with torch.cuda.device(dev):
-        _check(fn(*(run + cache + at if write else cache + at + run), B, T, W, Hkv, D, _dtype_code(k),
-                  _stream(stream)), name)
+    args = run + cache + at if write else cache + at + run
+    _check(_on(dev, stream, lambda st: fn(*args, B, T, W, Hkv, D, _dtype_code(k), st)), name)
 
 
 def swa_kv8_write(k, v, k8, k_exp, v8, v_exp, pos, count=None, stream=None) -> None:
@@ -445,11 +453,10 @@ def swa_decode_kv8(q, k_new, v_new, k8, k_exp, v8, v_exp, pos, out, workspace=No
     Bc, W, Hkv, Dc = _cache8(k8, k_exp, v8, v_exp)
     dev, B, Hq, D = _step_args(q, k_new, v_new, pos, out, Hkv, k8, k_exp, v8, v_exp)
     _like("k8", k8, (B, W, Hkv, D), torch.float8_e4m3fn)
-    with torch.cuda.device(dev):
-        workspace = _scratch(workspace, swa_decode_kv8_workspace_bytes(B, Hq, Hkv, D, W), dev, stream)
-        _check(_lib.swa_decode_kv8(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k8), _ptr(k_exp), _ptr(v8), _ptr(v_exp),
-                                   _ptr(pos), W, B, Hq, Hkv, D, _ptr(out), _ptr(workspace), workspace.nbytes,
-                                   _dtype_code(q), _stream(stream)), "swa_decode_kv8")
+    ws = _scratch(workspace, _lib.swa_decode_kv8_workspace_bytes(B, Hq, Hkv, D, W), dev, stream)
+    _check(_on(dev, stream, lambda st: _lib.swa_decode_kv8(
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k8), _ptr(k_exp), _ptr(v8), _ptr(v_exp), _ptr(pos), W, B, Hq, Hkv, D,
+        _ptr(out), _ptr(ws), ws.nbytes, _dtype_code(q), st)), "swa_decode_kv8")
     return out
 
 
@@ -462,12 +469,10 @@ def swa_decode_prefix(q, k_new, v_new, k_prefix, v_prefix, k_cache, v_cache, pos
     for what, t, shape in (("k_cache", k_cache, (B, W, Hkv, D)), ("v_cache", v_cache, (B, W, Hkv, D)),
                            ("k_prefix", k_prefix, (N, Hkv, D)), ("v_prefix", v_prefix, (N, Hkv, D))):
         _like(what, t, shape, q.dtype)
-    with torch.cuda.device(dev):
-        workspace = _scratch(workspace, swa_decode_prefix_workspace_bytes(B, Hq, Hkv, D, W, N), dev, stream)
-        _check(_lib.swa_decode_prefix(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_prefix), _ptr(v_prefix), N,
-                                      _ptr(k_cache), _ptr(v_cache), _ptr(pos), W, B, Hq, Hkv, D, _ptr(out),
-                                      _ptr(workspace), workspace.nbytes, _dtype_code(q), _stream(stream)),
-               "swa_decode_prefix")
+    ws = _scratch(workspace, _lib.swa_decode_prefix_workspace_bytes(B, Hq, Hkv, D, W, N), dev, stream)
+    _check(_on(dev, stream, lambda st: _lib.swa_decode_prefix(
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_prefix), _ptr(v_prefix), N, _ptr(k_cache), _ptr(v_cache), _ptr(pos),
+        W, B, Hq, Hkv, D, _ptr(out), _ptr(ws), ws.nbytes, _dtype_code(q), st)), "swa_decode_prefix")
     return out
 
 
@@ -483,12 +488,11 @@ def swa_decode_sparse(q, k_new, v_new, k_cache, v_cache, bounds, pos, out, selec
         _like(what, t, (B, W, Hkv, D), q.dtype)
     _like("bounds", bounds, (B, Hkv, -(-W // max(1, block)), 2, D), q.dtype)
     _like("selected", selected, (B, Hkv, selected.shape[-1]), torch.int32)
-    with torch.cuda.device(dev):
-        workspace = _scratch(workspace, swa_decode_sparse_workspace_bytes(B, Hq, Hkv, D, W, block), dev, stream)
-        _check(_lib.swa_decode_sparse(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(bounds),
-                                      _ptr(pos), W, block, selected.shape[-1], n_first, n_last, B, Hq, Hkv, D,
-                                      _ptr(out), _ptr(selected), _ptr(workspace), workspace.nbytes, _dtype_code(q),
-                                      _stream(stream)), "swa_decode_sparse")
+    ws = _scratch(workspace, _lib.swa_decode_sparse_workspace_bytes(B, Hq, Hkv, D, W, block), dev, stream)
+    _check(_on(dev, stream, lambda st: _lib.swa_decode_sparse(
+        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(bounds), _ptr(pos), W, block,
+        selected.shape[-1], n_first, n_last, B, Hq, Hkv, D, _ptr(out), _ptr(selected), _ptr(ws), ws.nbytes,
+        _dtype_code(q), st)), "swa_decode_sparse")
     return out
 
 
@@ -498,9 +502,8 @@ def swa_block_bounds(k_cache, pos, bounds, block: int, stream=None) -> torch.Ten
     B, W, Hkv, D = k_cache.shape
     _like("pos", pos, (B,), torch.int64)
     _like("bounds", bounds, (B, Hkv, -(-W // max(1, block)), 2, D), k_cache.dtype)
-    with torch.cuda.device(_cuda(k_cache, pos, bounds)):
-        _check(_lib.swa_block_bounds(_ptr(k_cache), _ptr(pos), _ptr(bounds), W, block, B, Hkv, D,
-                                     _dtype_code(k_cache), _stream(stream)), "swa_block_bounds")
+    _check(_on(_cuda(k_cache, pos, bounds), stream, lambda st: _lib.swa_block_bounds(
+        _ptr(k_cache), _ptr(pos), _ptr(bounds), W, block, B, Hkv, D, _dtype_code(k_cache), st)), "swa_block_bounds")
     return bounds
 
 

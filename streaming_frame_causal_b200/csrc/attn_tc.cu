@@ -253,6 +253,39 @@ SWA_DEV Work decode_work(const TcParams& p, const int* tpre) {
   return w;
 }
 
+// A shared prefix (launch_prefix_tc): the rows of a query tile are whole groups of a
+// KV head's G query heads, (sequence, head) in order, as many as 128 rows hold; the
+// keys are the N tokens of the prefix, and every item writes a partial.
+SWA_DEV int prefix_rows(const TcParams& p) {
+  const int G = p.Hq / p.Hkv;
+  return G * (kRows / G);
+}
+
+SWA_DEV Work prefix_work(const TcParams& p) {
+  Work w;
+  w.grow = nullptr;
+  w.glen = nullptr;
+  w.tpre = nullptr;
+  w.srow1 = w.slen1 = 0;
+  const int bid = static_cast<int>(blockIdx.x), items = p.Hkv * p.n_pairs;
+  const int split = bid / items, it = bid - split * items;
+  const int pair = it / p.Hkv, rt = prefix_rows(p);
+  w.b = 0;
+  w.kvh = it - pair * p.Hkv;
+  w.h0 = w.h1 = w.kvh;
+  w.qrow0 = 2 * pair * rt;
+  w.qrow1 = w.qrow0 + rt;
+  const int rows = p.B * (p.Hq / p.Hkv);
+  w.rows0 = imin(rt, rows - w.qrow0);
+  w.rows1 = imax(0, imin(rt, rows - w.qrow1));
+  w.nseg = 1;
+  w.srow0 = 0;
+  w.slen0 = p.Nq;
+  w.split = split;
+  split_range(cdiv(p.Nq, kRows), p.splits, split, &w.t_begin, &w.t_end);
+  return w;
+}
+
 // How the 64 exponential pairs of a 128-column row are split (per group of 8 pairs):
 // the first kPolyPairs take 2^x on the FMA pipe (polynomial), the rest two f32
 // MUFU exp2.  Measured on B200 with the warp issuer (same-box A/B): at head_dim
@@ -274,7 +307,7 @@ SWA_DEV float max3f(float a, float b, float c) {
   return d;
 }
 
-template <int D>
+template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ TcParams p) {
   using PL = Plan<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -386,7 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + PL::kOffTmem);
-  const Work w = decode_work(p, tpre);
+  Work w;
+  if constexpr (PREFIX) w = prefix_work(p);
+  else w = decode_work(p, tpre);
   const int T = w.t_end - w.t_begin;
   const bool has_b = w.rows1 > 0;
   if (warp < 4) {
@@ -403,8 +438,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       if (is_k) {
         tma_prefetch_desc(&p.tm_q);
         for (int g = 0; g < (has_b ? 2 : 1); ++g) {
-          mbar_arrive_expect_tx(q_full(g), PL::kTileBytes);
+          mbar_arrive_expect_tx(q_full(g), PREFIX ? prefix_rows(p) * D * 2 : PL::kTileBytes);
           for (int sub = 0; sub < PL::kSubs; ++sub)
+            if constexpr (PREFIX)
+              tma_load_4d(base + PL::kOffQ + g * PL::kTileBytes + sub * kSubBytes, &p.tm_q, q_full(g), sub * 64, 0,
+                          w.kvh, (g ? w.qrow1 : w.qrow0) / (p.Hq / p.Hkv));
+            else
             tma_load_4d(base + PL::kOffQ + g * PL::kTileBytes + sub * kSubBytes, &p.tm_q, q_full(g),
                         sub * 64, g ? w.h1 : w.h0, g ? w.qrow1 : w.qrow0, w.b);
         }
@@ -774,9 +813,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const bool store = r < my_rows;
         const int row = my_row0 + r;
         const float inv = 1.f / l;
-        const int64_t idx = (w.split < 0)
+        int64_t idx = (w.split < 0)
                                 ? (static_cast<int64_t>(w.b) * p.Nq + row) * p.Hq + my_h
                                 : (static_cast<int64_t>(w.split) * p.Nq + row) * p.Hq + my_h;
+        if constexpr (PREFIX) {
+          const int G = p.Hq / p.Hkv;
+          idx = (static_cast<int64_t>(w.split) * p.B + row / G) * p.Hq + w.kvh * G + row % G;
+        }
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t orr[32];
@@ -811,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           p.part_ml[idx * 2 + 1] = l;
         }
       }
-    } else if (T == 0 && w.split >= 0 && (g == 0 || has_b) && r < my_rows) {
+    } else if (!PREFIX && T == 0 && w.split >= 0 && (g == 0 || has_b) && r < my_rows) {
       // empty split: contributes nothing to the combine
       const int row = my_row0 + r;
       const int64_t idx = (static_cast<int64_t>(w.split) * p.Nq + row) * p.Hq + my_h;
@@ -820,6 +863,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
   }
 
+  // the prefix reads nothing that the kernel ahead of it writes, but those behind it
+  // do: they may start once this grid has ended, so it ends after that kernel
+  if constexpr (PREFIX) griddep_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -918,7 +964,7 @@ int tc_smem_bytes(int head_dim) {
 }
 
 namespace {
-template <int D>
+template <int D, bool PREFIX>
 cudaError_t launch_tc_d(const TcParams& p, int64_t n_items, cudaStream_t stream) {
   static DeviceOnce attr_set;  // devices on which the smem opt-in was set
   int dev = 0;
@@ -928,23 +974,61 @@ cudaError_t launch_tc_d(const TcParams& p, int64_t n_items, cudaStream_t stream)
     // with; refuse to launch a build whose pool would be too small (the
     // increasing warpgroups would otherwise wait forever)
     cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, attn_tc_kernel<D>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, attn_tc_kernel<D, PREFIX>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs * 12 < 4 * kRegsCtl + 8 * kRegsSoftmax) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<D>::kSmemBytes);
+    e = cudaFuncSetAttribute(attn_tc_kernel<D, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Plan<D>::kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set.mark(dev);
   }
-  attn_tc_kernel<D><<<static_cast<unsigned>(n_items), kThreads, Plan<D>::kSmemBytes, stream>>>(p);
   count_launches(1);
+  if constexpr (PREFIX)
+    return launch_after(attn_tc_kernel<D, PREFIX>, dim3(static_cast<unsigned>(n_items)), dim3(kThreads),
+                        Plan<D>::kSmemBytes, stream, p);
+  attn_tc_kernel<D, PREFIX><<<static_cast<unsigned>(n_items), kThreads, Plan<D>::kSmemBytes, stream>>>(p);
   return cudaGetLastError();
 }
 }  // namespace
 
 cudaError_t launch_attn_tc(const TcParams& p, int head_dim, int64_t n_items, cudaStream_t stream) {
   if (n_items <= 0) return cudaSuccess;
-  if (head_dim == 64) return launch_tc_d<64>(p, n_items, stream);
-  if (head_dim == 128) return launch_tc_d<128>(p, n_items, stream);
+  if (head_dim == 64) return launch_tc_d<64, false>(p, n_items, stream);
+  if (head_dim == 128) return launch_tc_d<128, false>(p, n_items, stream);
+  return cudaErrorInvalidValue;
+}
+
+int prefix_tc_items(int B, int G, int Hkv) {
+  const int rows = G * (kRows / G);
+  return Hkv * cdiv(cdiv(B * G, rows), 2);
+}
+
+cudaError_t launch_prefix_tc(const void* q, const void* k, const void* v, int N, int B, int Hq, int Hkv, int head_dim,
+                             int splits, float scale_log2, float* part_o, float* part_ml, int* err,
+                             cudaStream_t stream) {
+  TcParams p{};
+  const int G = Hq / Hkv;
+  const uint64_t D = static_cast<uint64_t>(head_dim);
+  const uint64_t dims[4] = {D, static_cast<uint64_t>(G), static_cast<uint64_t>(Hkv), static_cast<uint64_t>(B)};
+  const uint64_t strides[3] = {D * 2, D * 2 * G, D * 2 * Hq};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(G), 1, static_cast<uint32_t>(kRows / G)};
+  if (!encode_tiled(&p.tm_q, 2, q, 4, dims, strides, box, 128) ||
+      !encode_4d_sw128(&p.tm_k, k, head_dim, Hkv, N, 1) || !encode_4d_sw128(&p.tm_v, v, head_dim, Hkv, N, 1))
+    return cudaErrorInvalidValue;
+  p.part_o = part_o;
+  p.part_ml = part_ml;
+  p.err = err;
+  p.mode = TC_FRAME;  // no mask but the end of the keys
+  p.B = B;
+  p.Nq = N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.n_pairs = prefix_tc_items(B, G, Hkv) / Hkv;
+  p.splits = splits;
+  p.scale_log2 = scale_log2;
+  const int64_t ctas = static_cast<int64_t>(prefix_tc_items(B, G, Hkv)) * splits;
+  if (head_dim == 64) return launch_tc_d<64, true>(p, ctas, stream);
+  if (head_dim == 128) return launch_tc_d<128, true>(p, ctas, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -54,6 +54,14 @@ cudaError_t launch_attn_tc(const TcParams& p, int head_dim, int64_t n_items, cud
 cudaError_t launch_combine(const float* part_o, const float* part_ml, void* out, int rows, int H, int splits,
                            int head_dim, int64_t out_ld, int out_h0, cudaStream_t stream);
 int tc_smem_bytes(int head_dim);
+// The rows of a batch of single query tokens (B sequences of Hq heads) against N tokens
+// k, v [N, Hkv, D] that all of them see: split-KV partials part_o [splits, B * Hq, D],
+// part_ml [splits, B * Hq, 2]; splits <= the key tiles.  A programmatic launch that
+// reads nothing the kernel ahead of it writes, and ends after it.
+int prefix_tc_items(int B, int G, int Hkv);  // CTAs of a split
+cudaError_t launch_prefix_tc(const void* q, const void* k, const void* v, int N, int B, int Hq, int Hkv, int head_dim,
+                             int splits, float scale_log2, float* part_o, float* part_ml, int* err,
+                             cudaStream_t stream);
 
 // ---------------------------------------------------------------- SIMT f32 path
 enum SimtMode : int { SIMT_FRAME = 0, SIMT_BAND = 1, SIMT_STREAM = 2, SIMT_DECODE = 3 };

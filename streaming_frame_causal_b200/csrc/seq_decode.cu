@@ -667,13 +667,27 @@ struct SeqLayout {
   size_t cum, share, part_o, part_ml, pre_o, pre_ml, score, q8, q_scale, bytes;
 };
 
-// Pieces of the prefix for the CUDA-core kernel: enough for three CTAs per SM.
-int prefix_pieces(const SeqParams& p) {
+// Pieces of the prefix.  CUDA cores: enough for three CTAs per SM.  Tensor cores: one
+// CTA per SM at a time, so the count that minimises waves x (key tiles of a piece + the
+// 7.5 tiles' time that a CTA spends outside its tiles).
+int prefix_pieces(const SeqParams& p, bool tc) {
   if (p.N == 0 || p.B == 0) return 0;
-  const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.Hkv;
-  const int64_t want = (3 * 148 + ctas - 1) / ctas;
-  const int tiles = cdiv(p.N, kSeqKeys);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, tiles, kSeqMaxSplits})));
+  const int tiles = cdiv(p.N, kSeqKeys), most = std::min(tiles, kSeqMaxSplits);
+  if (!tc) {
+    const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.Hkv;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((3 * 148 + ctas - 1) / ctas, most)));
+  }
+  const int64_t items = prefix_tc_items(p.B, p.G, p.Hkv);
+  int best = 1;
+  double best_cost = 1e300;
+  for (int s = 1; s <= most; ++s) {
+    const double cost = static_cast<double>((items * s + 147) / 148) * (cdiv(tiles, s) + 7.5);
+    if (cost < best_cost - 1e-9) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 SeqLayout seq_layout(const SeqParams& p, int D, bool kv8) {
@@ -713,7 +727,7 @@ swa_status seq_sizes(SeqParams& p, int D, int dtype) {
       static_cast<int64_t>(p.B) * (p.W / kSeqKeys + 2) > 0x7fffffffll ||
       static_cast<int64_t>(p.W) * p.Hkv * D > (1ll << 37))
     return SWA_ERR_SHAPE;
-  p.splits = prefix_pieces(p);
+  p.splits = prefix_pieces(p, dtype == SWA_BF16);
   return SWA_OK;
 }
 
@@ -745,12 +759,17 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
       launches += 2;
     }
     if (e == cudaSuccess && p.N > 0) {
-      static DeviceOnce once;
-      e = allow_smem(prefix_simt_kernel<T, D>, SimtPlan<D>::kSmem, once);
-      const dim3 grid(static_cast<unsigned>(p.B * p.groups), p.Hkv, p.splits);
-      if (e == cudaSuccess)
-        e = launch_after(prefix_simt_kernel<T, D>, grid, dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
-      ++launches;
+      if constexpr (kTc) {
+        e = launch_prefix_tc(p.q, p.k_prefix, p.v_prefix, p.N, p.B, p.Hq, p.Hkv, D, p.splits, p.scale_log2, p.pre_o,
+                             p.pre_ml, p.err, st);
+      } else {
+        static DeviceOnce once;
+        e = allow_smem(prefix_simt_kernel<T, D>, SimtPlan<D>::kSmem, once);
+        const dim3 grid(static_cast<unsigned>(p.B * p.groups), p.Hkv, p.splits);
+        if (e == cudaSuccess)
+          e = launch_after(prefix_simt_kernel<T, D>, grid, dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
+        ++launches;
+      }
     }
   }
   if constexpr (kTc) {
@@ -826,8 +845,10 @@ bool block_size(int block) { return block == 16 || block == 32 || block == 64 ||
 
 // the workspace of a step of these sizes: enough for either type
 size_t workspace_of(SeqParams p, int D, bool kv8) {
-  if (p.B < 1 || seq_sizes(p, D, SWA_F32) != SWA_OK) return 0;
-  return seq_layout(p, D, kv8).bytes;
+  size_t most = 0;
+  for (const int dtype : {SWA_F32, SWA_BF16})
+    if (p.B > 0 && seq_sizes(p, D, dtype) == SWA_OK) most = std::max(most, seq_layout(p, D, kv8).bytes);
+  return most;
 }
 
 }  // namespace
