@@ -27,159 +27,118 @@ SWA_DEV float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 SWA_DEV void put_f32(float* p, float v) { *p = v; }
 SWA_DEV void put_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// ---------------------------------------------------------------- append and division
-// Block 0 divides the tiles; the warps of the other blocks take (sequence, KV head)
-// rows: the new token's K and V into slot pos mod W (as they are, or in 8 bits).
-// Block-sparse: the warp also renews the bounds of the block that the token entered,
-// from all its valid keys (the slot's old key may have been one of the extremes);
-// the new key comes from k_new, so nothing waits for the write above.
+// ---------------------------------------------------------------- division and append
 constexpr int kPrepThreads = 256;
 constexpr int kPrepWarps = kPrepThreads / 32;
 
+// one block: the sequences' tiles summed, and every team's share of their line
+SWA_DEV void seq_divide(const SeqParams& p) {
+  __shared__ int sums[kPrepWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
+    const int b = b0 + threadIdx.x;
+    const int v = b < p.B ? seq_tiles(p, b) : 0;
+    int s = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, off);
+      if (lane >= off) s += y;
+    }
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < kPrepWarps; ++w) {
+      if (w < warp) before += sums[w];
+      carry += sums[w];
+    }
+    if (b < p.B) p.cum[b] = before + s - v;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) p.cum[p.B] = carry;
+  __syncthreads();
+  const int teams = seq_teams(p, carry);
+  for (int c = threadIdx.x; c < p.teams; c += kPrepThreads) {
+    int4 s = make_int4(0, 0, 0, 0);
+    if (c < teams) {
+      const int t = static_cast<int>(static_cast<int64_t>(carry) * c / teams);
+      const int end = static_cast<int>(static_cast<int64_t>(carry) * (c + 1) / teams);
+      int lo = 0, hi = p.B;  // the last b whose tiles begin at t or before it
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cum[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      s = make_int4(lo, t - p.cum[lo], end - t, 0);
+    }
+    p.share[c] = s;
+  }
+}
+
+// Block 0 divides the work; the warps of the other blocks take a row each: the new
+// token's K or V of one (sequence, KV head) into slot pos mod W, as it is or in 8 bits,
+// or one query head's two e4m3 terms for the tensor cores (seq_tc.cu).
 template <typename T, int D, int KIND>
 __global__ void __launch_bounds__(kPrepThreads) seq_prep_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0) {
-    __shared__ int sums[kPrepWarps + 1];
-    int carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
-      const int b = b0 + threadIdx.x;
-      const int v = b < p.B ? seq_tiles(p, b) : 0;
-      int s = v;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += y;
-      }
-      if (lane == 31) sums[warp] = s;
-      __syncthreads();
-      int before = carry, all = carry;
-      for (int w = 0; w < kPrepWarps; ++w) {
-        if (w < warp) before += sums[w];
-        all += sums[w];
-      }
-      if (b < p.B) p.cum[b] = before + s - v;
-      carry = all;
-      __syncthreads();
-    }
-    if (threadIdx.x == 0) p.cum[p.B] = carry;
-    __syncthreads();
-    const int64_t total = static_cast<int64_t>(carry) * p.items;
-    const int ctas = seq_ctas(p, total);
-    for (int c = threadIdx.x; c < p.ctas; c += kPrepThreads) {
-      int4 s = make_int4(0, 0, 0, 0);
-      if (c < ctas) {
-        const int64_t t = total * c / ctas, end = total * (c + 1) / ctas;
-        int lo = 0, hi = p.B;  // the last b whose tiles begin at t or before it
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (static_cast<int64_t>(p.cum[mid]) * p.items <= t) lo = mid;
-          else hi = mid;
-        }
-        const int of = p.cum[lo + 1] - p.cum[lo];
-        const int64_t r = t - static_cast<int64_t>(p.cum[lo]) * p.items;
-        s = make_int4(lo, static_cast<int>(r / of), static_cast<int>(r % of), static_cast<int>(end - t));
-      }
-      p.share[c] = s;
-    }
+    seq_divide(p);
     return;
   }
   constexpr int E = D / 32;  // elements of a lane
-  constexpr bool kSplitQ = KIND == SEQ_KV8 && sizeof(T) == 2;  // for the tensor cores (seq_tc.cu)
-  const int64_t row = static_cast<int64_t>(blockIdx.x - 1) * kPrepWarps + warp;
+  constexpr bool kSplitQ = KIND == SEQ_KV8 && sizeof(T) == 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_row = kSplitQ ? 2 + p.G : 2;
+  const int64_t job = static_cast<int64_t>(blockIdx.x - 1) * kPrepWarps + warp;
+  const int64_t row = job / per_row;
+  const int what = static_cast<int>(job - row * per_row);  // K, V, query heads
   if (row >= static_cast<int64_t>(p.B) * p.Hkv) return;
   const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<int64_t>(b) * p.Hkv);
+  const T* src = static_cast<const T*>(what == 0 ? p.k_new : p.v_new) + row * D + lane * E;
+  if (what >= 2) src = static_cast<const T*>(p.q) + (row * p.G + what - 2) * D + lane * E;
+  T x[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = src[i];
   const long long pos = p.pos[b];
   if (pos < 0) return;
   const int slot = static_cast<int>(pos % p.W);
   const int64_t at = ((static_cast<int64_t>(b) * p.W + slot) * p.Hkv + h) * D + lane * E;
-  float kn[E];
-  for (int kv = 0; kv < 2; ++kv) {
-    const T* src = static_cast<const T*>(kv ? p.v_new : p.k_new) + row * D + lane * E;
-    float x[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = to_f32(src[i]);
-    if (kv == 0)
-#pragma unroll
-      for (int i = 0; i < E; ++i) kn[i] = x[i];
-    if constexpr (KIND == SEQ_KV8) {
-      float a = 0.f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) a = fmaxf(a, fabsf(x[i]));
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-      const int e = kv8_exponent(a);
-      uint8_t* dst = static_cast<uint8_t*>(kv ? p.v_cache : p.k_cache) + at;
-#pragma unroll
-      for (int i = 0; i < E; ++i) dst[i] = static_cast<uint8_t>(to_e4m3x2(x[i] * pow2i(-e), 0.f));
-      if (lane == 0)
-        (kv ? p.v_exp : p.k_exp)[(static_cast<int64_t>(b) * p.Hkv + h) * p.W + slot] = static_cast<uint8_t>(e + 127);
-    } else {
-      T* dst = static_cast<T*>(kv ? p.v_cache : p.k_cache) + at;
-#pragma unroll
-      for (int i = 0; i < E; ++i) dst[i] = src[i];
-    }
-  }
-  if constexpr (kSplitQ) {
-    // query head g as hi in row g and lo in row columns + g of the item's 16 rows
-    const int cols = seq_head_columns(p.G);
-    uint8_t* dst = p.q8 + row * kSeqCols * D + lane * E;
-    for (int g = 0; g < kSeqCols; ++g) {
-      if (g < cols && g < p.G) {
-        const int64_t qrow = static_cast<int64_t>(b) * p.Hq + h * p.G + g;
-        const T* src = static_cast<const T*>(p.q) + qrow * D + lane * E;
-        float x[E], a = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          x[i] = to_f32(src[i]);
-          a = fmaxf(a, fabsf(x[i]));
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-        const int e = min(max(exponent448(a), -118), 118);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float y = x[i] * pow2i(-e);
-          const uint32_t hi = to_e4m3x2(y, 0.f);
-          dst[g * D + i] = static_cast<uint8_t>(hi);
-          dst[(cols + g) * D + i] = static_cast<uint8_t>(to_e4m3x2(y - from_e4m3x2(hi).x, 0.f));
-        }
-        // an infinite query has no softmax: its scores become NaN
-        if (lane == 0) p.q_scale[qrow] = a == INFINITY ? NAN : pow2i(e);
-      } else if (g < cols) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) dst[g * D + i] = dst[(cols + g) * D + i] = 0;
-      } else if (g >= 2 * cols) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) dst[g * D + i] = 0;
-      }
-    }
-  }
   if constexpr (KIND == SEQ_PLAIN) {
-    if (p.block == 0) return;
-    const int blk = slot / p.block, n = seq_tokens(p, b);
-    const int end = min(blk * p.block + p.block, n);
-    float lo[E], hi[E];
+    T* dst = static_cast<T*>(what == 0 ? p.k_cache : p.v_cache) + at;
 #pragma unroll
-    for (int i = 0; i < E; ++i) lo[i] = hi[i] = kn[i];
-    const T* k = static_cast<const T*>(p.k_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + lane * E;
-#pragma unroll 8
-    for (int s = blk * p.block; s < end; ++s) {
-      if (s == slot) continue;
-      const T* r = k + static_cast<int64_t>(s) * p.Hkv * D;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float x = to_f32(r[i]);
-        lo[i] = fminf(lo[i], x);
-        hi[i] = fmaxf(hi[i], x);
-      }
-    }
-    T* o = static_cast<T*>(p.bounds) + (row * p.n_blocks + blk) * 2 * D + lane * E;
+    for (int i = 0; i < E; ++i) dst[i] = x[i];
+  } else {
+    float f[E], a = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      put_f32(o + i, lo[i]);
-      put_f32(o + D + i, hi[i]);
+      f[i] = to_f32(x[i]);
+      a = fmaxf(a, fabsf(f[i]));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    if (what < 2) {
+      const int e = kv8_exponent(a);
+      uint8_t* dst = static_cast<uint8_t*>(what == 0 ? p.k_cache : p.v_cache) + at;
+#pragma unroll
+      for (int i = 0; i < E; ++i) dst[i] = static_cast<uint8_t>(to_e4m3x2(f[i] * pow2i(-e), 0.f));
+      if (lane == 0)
+        (what == 0 ? p.k_exp : p.v_exp)[(static_cast<int64_t>(b) * p.Hkv + h) * p.W + slot] =
+            static_cast<uint8_t>(e + 127);
+    } else {
+      // query head g as hi in row g and lo in row columns + g of the item's 16 rows (those
+      // between and behind them stay as they are: their columns are never read)
+      const int g = what - 2, cols = seq_head_columns(p.G);
+      const int e = min(max(exponent448(a), -118), 118);
+      uint8_t* dst = p.q8 + row * kSeqCols * D + lane * E;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float y = f[i] * pow2i(-e);
+        const uint32_t hi = to_e4m3x2(y, 0.f);
+        dst[g * D + i] = static_cast<uint8_t>(hi);
+        dst[(cols + g) * D + i] = static_cast<uint8_t>(to_e4m3x2(y - from_e4m3x2(hi).x, 0.f));
+      }
+      // an infinite query has no softmax: its scores become NaN
+      if (lane == 0) p.q_scale[row * p.G + g] = a == INFINITY ? NAN : pow2i(e);
     }
   }
 }
@@ -225,6 +184,9 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const SeqParams p) {
 }
 
 // ---------------------------------------------------------------- block scores
+// The new token enters the cache, the bounds of its block are renewed, and the blocks'
+// scores are formed, with the division of the work beside them (one more block).
+//
 // score(j) = sum over the group's query heads and the elements of max(q low_j, q high_j),
 // the sum over the heads of a bound that no key of the block exceeds.  With
 // up = sum_g max(q_g, 0) and down = sum_g min(q_g, 0) it is up . high_j + down . low_j,
@@ -232,81 +194,167 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const SeqParams p) {
 // more of them than the products of 16-bit values fill), so that blocks are ordered
 // as the definition orders them and only ties go to the lower index: in 32 bits two
 // near scores may change places, and with them what the step attends to.
+//
+// Bound: the bounds' bytes.  A CTA takes 64 blocks of one (sequence, KV head); lanes
+// hold 16 bytes of a row each, and their part of up and down in registers.  The
+// CTA that holds the token's block first renews its bounds from all its valid keys
+// (the slot's old key may have been one of the extremes).
 SWA_DEV uint64_t sortable(double x) {
   if (isnan(x)) return 0;  // behind every number
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));  // -0 as +0
   return (u >> 63) ? ~u : u | (1ull << 63);
 }
 
-constexpr int kScoreThreads = 256;
+constexpr int kScoreThreads = kPrepThreads;
 constexpr int kScoreBlocks = 64;  // cache blocks of a CTA
+
+// 16 bytes of a row in 32 bits
+template <typename T>
+SWA_DEV void load16(const T* x, float* v) {
+  if constexpr (sizeof(T) == 2) {
+    load8(x, v);
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(x);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
-  constexpr int E = D / 32;
-  __shared__ double up[D], down[D];
-  const int64_t row = blockIdx.y;  // (b, KV head)
-  const int b = static_cast<int>(row / p.Hkv);
+  constexpr int E = 16 / sizeof(T);       // elements of a lane
+  constexpr int kLanes = D / E;           // lanes of a row
+  constexpr int kRows = kScoreThreads / kLanes;
+  const int chunks = (p.n_blocks + kScoreBlocks - 1) / kScoreBlocks;
+  if (blockIdx.x == 0) {
+    seq_divide(p);
+    return;
+  }
+  const int64_t u = blockIdx.x - 1;
+  const int64_t row = u / chunks;  // (b, KV head)
+  const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<int64_t>(b) * p.Hkv);
+  const int j0 = static_cast<int>(u - row * chunks) * kScoreBlocks;
   const int n = seq_tokens(p, b);
   const int used = n > 0 ? (n + p.block - 1) / p.block : 0;
-  const T* q = static_cast<const T*>(p.q) + row * p.G * D;
-  if (threadIdx.x < D) {
-    double u = 0.0, d = 0.0;
-    for (int g = 0; g < p.G; ++g) {
-      const double x = static_cast<double>(to_f32(q[g * D + threadIdx.x]));
-      // a NaN fails both comparisons and goes to both sums
-      u += x < 0.0 ? 0.0 : x;
-      d += x > 0.0 ? 0.0 : x;
+  if (j0 >= used) return;
+  const int slot = static_cast<int>(p.pos[b] % p.W), newest = slot / p.block;
+  const int part = threadIdx.x % kLanes, r = threadIdx.x / kLanes;
+  T* bounds = static_cast<T*>(p.bounds) + row * p.n_blocks * 2 * D + part * E;
+  if (newest >= j0 && newest < j0 + kScoreBlocks) {
+    __shared__ float low[kRows][D], high[kRows][D];
+    const T* kn = static_cast<const T*>(p.k_new) + row * D + part * E;
+    const T* vn = static_cast<const T*>(p.v_new) + row * D + part * E;
+    T* k = static_cast<T*>(p.k_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + part * E;
+    T* v = static_cast<T*>(p.v_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + part * E;
+    const int64_t step = static_cast<int64_t>(p.Hkv) * D;
+    float lo[E], hi[E], x[E];
+    load16(kn, x);
+#pragma unroll
+    for (int i = 0; i < E; ++i) lo[i] = hi[i] = x[i];
+    const int end = min(newest * p.block + p.block, n);
+#pragma unroll 4
+    for (int s = newest * p.block + r; s < end; s += kRows) {
+      load16(s == slot ? kn : k + s * step, x);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        lo[i] = fminf(lo[i], x[i]);
+        hi[i] = fmaxf(hi[i], x[i]);
+      }
     }
-    up[threadIdx.x] = u;
-    down[threadIdx.x] = d;
-  }
-  __syncthreads();
-  griddep_wait();  // the bounds of the newest block
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int newest = n > 0 ? static_cast<int>(p.pos[b] % p.W) / p.block : 0;
-  const int j0 = blockIdx.x * kScoreBlocks;
-  for (int j = j0 + warp; j < min(j0 + kScoreBlocks, used); j += kScoreThreads / 32) {
-    const T* r = static_cast<const T*>(p.bounds) + (row * p.n_blocks + j) * 2 * D + lane * E;
-    double s = 0.0;
+    if (r == 0) {
+      *reinterpret_cast<uint4*>(k + slot * step) = *reinterpret_cast<const uint4*>(kn);
+      *reinterpret_cast<uint4*>(v + slot * step) = *reinterpret_cast<const uint4*>(vn);
+    }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      s += up[lane * E + i] * static_cast<double>(to_f32(r[D + i]));
-      s += down[lane * E + i] * static_cast<double>(to_f32(r[i]));
+      low[r][part * E + i] = lo[i];
+      high[r][part * E + i] = hi[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float a = low[0][threadIdx.x], c = high[0][threadIdx.x];
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) {
+        a = fminf(a, low[i][threadIdx.x]);
+        c = fmaxf(c, high[i][threadIdx.x]);
+      }
+      T* o = static_cast<T*>(p.bounds) + (row * p.n_blocks + newest) * 2 * D + threadIdx.x;
+      put_f32(o, a);
+      put_f32(o + D, c);
+    }
+    __syncthreads();
+  }
+  double up[E], down[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) up[i] = down[i] = 0.0;
+  for (int g = 0; g < p.G; ++g) {
+    float x[E];
+    load16(static_cast<const T*>(p.q) + (row * p.G + g) * D + part * E, x);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      // a NaN fails both comparisons and goes to both sums
+      up[i] += x[i] < 0.f ? 0.0 : static_cast<double>(x[i]);
+      down[i] += x[i] > 0.f ? 0.0 : static_cast<double>(x[i]);
+    }
+  }
+  // all threads take part in the sums over a row's lanes, with or without a block of their own
+#pragma unroll 2
+  for (int i0 = 0; i0 < kScoreBlocks; i0 += kRows) {
+    const int j = j0 + i0 + r;
+    if (j0 + i0 >= used) break;
+    double s = 0.0;
+    if (i0 + r < kScoreBlocks && j < used) {
+      float lo[E], hi[E];
+      load16(bounds + static_cast<int64_t>(j) * 2 * D, lo);
+      load16(bounds + static_cast<int64_t>(j) * 2 * D + D, hi);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        s += up[i] * static_cast<double>(hi[i]);
+        s += down[i] * static_cast<double>(lo[i]);
+      }
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    for (int off = kLanes / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     const int back = newest >= j ? newest - j : newest - j + used;
-    if (lane == 0) p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last) ? ~0ull : sortable(s);
+    if (part == 0 && i0 + r < kScoreBlocks && j < used)
+      p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last) ? ~0ull : sortable(s);
   }
 }
 
 // ---------------------------------------------------------------- selection
 // The n_select greatest scores of a row, ties to the lower index, their indices in
 // ascending order: the threshold is found a byte at a time from the top (a histogram
-// of the scores that agree with the bytes found so far), then one ordered pass
-// writes what is above it and the first of what equals it.
+// of the scores that agree with the bytes found so far, summed from its upper end by
+// all threads), until a bin is wanted whole; then one ordered pass writes what is above
+// the threshold and the first of what equals it.
 constexpr int kSelThreads = 256;
+constexpr int kSelKeep = 2048;  // scores kept in shared memory
 
 __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
-  griddep_wait();
+  __shared__ uint64_t keep[kSelKeep];
   __shared__ int hist[256];
   __shared__ int wsum[2][kSelThreads / 32];
-  __shared__ int s_bin, s_want;
+  __shared__ int s_bin, s_want, s_whole;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x;
   const int b = static_cast<int>(row / p.Hkv);
   const int n = seq_tokens(p, b);
   const int used = n > 0 ? (n + p.block - 1) / p.block : 0;
   int* sel = p.selected + row * p.n_select;
   const int take = min(used, p.n_select);
+  griddep_wait();  // the scores; and an earlier step may still read the selection
   for (int i = take + threadIdx.x; i < p.n_select; i += kSelThreads) sel[i] = -1;
   if (used <= p.n_select) {
     for (int i = threadIdx.x; i < used; i += kSelThreads) sel[i] = i;
     return;
   }
   const uint64_t* score = p.score + row * p.n_blocks;
+  if (used <= kSelKeep) {
+    for (int j = threadIdx.x; j < used; j += kSelThreads) keep[j] = score[j];
+    score = keep;
+    __syncthreads();
+  }
   uint64_t found = 0, mask = 0;
   int want = take;  // scores still to be found among those that agree with `found`
   for (int shift = 56; shift >= 0; shift -= 8) {
@@ -317,26 +365,35 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
       if ((s & mask) == found) atomicAdd(&hist[(s >> shift) & 255], 1);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int bin = 255, left = want;
-      while (hist[bin] < left) left -= hist[bin--];
-      s_bin = bin;
-      s_want = left;
+    // thread t: bin 255 - t, the scores in it and in all above it
+    const int mine = hist[255 - threadIdx.x];
+    int sum = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += y;
+    }
+    if (lane == 31) wsum[0][warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += wsum[0][w];
+    if (sum >= want && sum - mine < want) {
+      s_bin = 255 - threadIdx.x;
+      s_want = want - (sum - mine);
+      s_whole = sum == want;
     }
     __syncthreads();
     found |= static_cast<uint64_t>(s_bin) << shift;
     mask |= 255ull << shift;
     want = s_want;
-    __syncthreads();
+    if (s_whole) break;  // the bin is wanted whole: no byte below it decides anything
   }
-  // above: every score greater than the threshold; of those equal to it the first `want`
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int above = 0, equal = 0;  // so far, over all threads
   for (int j0 = 0; j0 < used; j0 += kSelThreads) {
     const int j = j0 + threadIdx.x;
-    const uint64_t s = j < used ? score[j] : 0;
+    const uint64_t s = j < used ? score[j] & mask : 0;
     const bool a = j < used && s > found, e = j < used && s == found;
     const unsigned ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
+    __syncthreads();  // the sums of the round before are read
     if (lane == 0) {
       wsum[0][warp] = __popc(ba);
       wsum[1][warp] = __popc(be);
@@ -352,7 +409,6 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_
       equal += wsum[1][w];
     }
     if (a || (e && xe < want)) sel[xa + min(xe, want)] = j;
-    __syncthreads();
   }
 }
 
@@ -521,10 +577,10 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
   st.bind(smem);
   SeqWalk walk;
   walk.start(p, blockIdx.x);
+  const int kvh = walk.item / p.groups, g0 = (walk.item - kvh * p.groups) * kSeqRows;
+  const int rows = min(kSeqRows, p.G - g0);
   SeqRun run;
-  while (walk.next(p, blockIdx.x, run)) {
-    const int kvh = run.item / p.groups, g0 = (run.item - kvh * p.groups) * kSeqRows;
-    const int rows = min(kSeqRows, p.G - g0);
+  while (walk.next(p, run)) {
     const int64_t qrow = static_cast<int64_t>(run.b) * p.Hq + kvh * p.G + g0;
     const int n = seq_tokens(p, run.b);
     st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
@@ -594,69 +650,109 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------- merge
-// One warp per (sequence, query head): sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over
-// the pieces of its item, in the order of the tiles, then the prefix's.  Items that
-// one CTA held whole are written already; an idle row's output is zero.
+// sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the pieces of a (sequence, query
+// head): those of its item in the order of the tiles, then the prefix's.  One warp, or up
+// to 8 where there are many pieces; a lane holds one piece's weight, and the warp adds
+// the pieces' outputs with independent loads.  Items that one CTA held whole are written
+// already; an idle row's output is zero.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) seq_merge_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
-  griddep_wait();
   constexpr int E = D / 32;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (u >= static_cast<int64_t>(p.B) * p.Hq) return;
-  const int b = static_cast<int>(u / p.Hq), h = static_cast<int>(u - static_cast<int64_t>(b) * p.Hq);
+  __shared__ float part[8][D + 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wi = warp % p.merge_warps;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * (8 / p.merge_warps) + warp / p.merge_warps;
+  const bool mine = u < static_cast<int64_t>(p.B) * p.Hq;
+  const int b = mine ? static_cast<int>(u / p.Hq) : 0, h = mine ? static_cast<int>(u - static_cast<int64_t>(b) * p.Hq) : 0;
   const int kvh = h / p.G, g = h - kvh * p.G;
   const int item = kvh * p.groups + g / kSeqRows, row = g % kSeqRows;
-  T* out = static_cast<T*>(p.out) + u * D + lane * E;
-  const int tiles = p.cum[b + 1] - p.cum[b];
-  if (tiles == 0) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) put_f32(out + i, 0.f);
-    return;
+  griddep_wait();
+  const int t = p.cum[b], tiles = p.cum[b + 1] - t, total = p.cum[p.B];
+  int pieces = 0, c0 = 0;
+  if (mine && tiles > 0) {
+    const int teams = seq_teams(p, total);
+    c0 = seq_owner(t, total, teams);
+    pieces = seq_owner(t + tiles - 1, total, teams) - c0 + 1;
   }
-  const int64_t total = static_cast<int64_t>(p.cum[p.B]) * p.items;
-  const int64_t t = static_cast<int64_t>(p.cum[b]) * p.items + static_cast<int64_t>(item) * tiles;
-  const int ctas = seq_ctas(p, total);
-  const int c0 = seq_owner(t, total, ctas), c1 = seq_owner(t + tiles - 1, total, ctas);
-  if (c0 == c1 && p.N == 0) return;
-  const int pieces = c1 - c0 + 1;
-  auto part = [&](int i, const float*& o, float& m, float& l) {
-    const float* ml;
-    if (i < pieces) {
-      const int64_t slot = pieces == 1 ? 2 * p.ctas + static_cast<int64_t>(b) * p.items + item
-                                       : (i == 0 ? 2 * c0 + 1 : 2 * (c0 + i));
-      o = p.part_o + (slot * kSeqRows + row) * D + lane * E;
-      ml = p.part_ml + (slot * kSeqRows + row) * 2;
-    } else {
-      const int64_t at = static_cast<int64_t>(i - pieces) * p.B * p.Hq + u;
-      o = p.pre_o + at * D + lane * E;
-      ml = p.pre_ml + at * 2;
-    }
-    m = ml[0];
-    l = ml[1];
-  };
+  const int all = pieces == 0 || (pieces == 1 && p.N == 0) ? 0 : pieces + p.splits;
   float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) acc[i] = 0.f;
-  const int all = pieces + p.splits;
-  const float* o;
-  float m, l;
-  for (int i = 0; i < all; ++i) {
-    part(i, o, m, l);
-    M = fmaxf(M, m);
-  }
-  for (int i = 0; i < all; ++i) {
-    part(i, o, m, l);
-    const float w = exp2f(m - M);
-    L += w * l;
+  for (int i0 = wi; i0 < all; i0 += 32 * p.merge_warps) {
+    const int i = i0 + lane * p.merge_warps;
+    const float *o = p.part_o, *ml = nullptr;
+    if (i < pieces) {
+      const int64_t slot = pieces == 1 ? 2 * p.ctas + static_cast<int64_t>(b) * p.items + item
+                                       : 2 * (static_cast<int64_t>(c0 + i) * p.items + item) + (i == 0 ? 1 : 0);
+      o = p.part_o + (slot * kSeqRows + row) * D;
+      ml = p.part_ml + (slot * kSeqRows + row) * 2;
+    } else if (i < all) {
+      const int64_t at = static_cast<int64_t>(i - pieces) * p.B * p.Hq + u;
+      o = p.pre_o + at * D;
+      ml = p.pre_ml + at * 2;
+    }
+    float m = -INFINITY, l = 0.f;
+    if (ml) {
+      const float2 v = *reinterpret_cast<const float2*>(ml);
+      m = v.x;
+      l = v.y;
+    }
+    float top = m;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += w * o[e];
-  }
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    top = fmaxf(top, M);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float w = exp2f(m - ref), keep = exp2f(M - ref);
+    float sum = w * l;
 #pragma unroll
-  for (int e = 0; e < E; ++e) put_f32(out + e, acc[e] / L);
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    L = L * keep + sum;
+    M = top;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= keep;
+    const int n = min(32, (all - i0 + p.merge_warps - 1) / p.merge_warps);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* ok =
+          reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k)) + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, ok[e], acc[e]);
+    }
+  }
+  if (p.merge_warps > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+    if (lane == 0) {
+      part[warp][D] = M;
+      part[warp][D + 1] = L;
+    }
+    __syncthreads();
+    if (wi != 0) return;
+    float top = -INFINITY;
+    for (int k = 0; k < p.merge_warps; ++k) top = fmaxf(top, part[warp + k][D]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k = 0; k < p.merge_warps; ++k) {
+      const float w = exp2f(part[warp + k][D] - ref);
+      L += w * part[warp + k][D + 1];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w * part[warp + k][lane * E + e];
+    }
+  }
+  if (!mine) return;
+  T* out = static_cast<T*>(p.out) + u * D + lane * E;
+  if (pieces == 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) put_f32(out + e, 0.f);
+  } else if (all > 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) put_f32(out + e, acc[e] / L);
+  }
 }
-
 
 // ---------------------------------------------------------------- host
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -698,7 +794,7 @@ SeqLayout seq_layout(const SeqParams& p, int D, bool kv8) {
     at += round256(bytes);
     return here;
   };
-  const size_t slots = 2 * kSeqMaxCtas + (p.N > 0 ? static_cast<size_t>(p.B) * p.items : 0);
+  const size_t slots = 2 * static_cast<size_t>(std::max(kSeqMaxCtas, p.items)) + (p.N > 0 ? static_cast<size_t>(p.B) * p.items : 0);
   const size_t pre = static_cast<size_t>(p.splits) * p.B * p.Hq;
   l.cum = take((static_cast<size_t>(p.B) + 1) * sizeof(int));
   l.share = take(kSeqMaxCtas * sizeof(int4));
@@ -744,20 +840,29 @@ cudaError_t allow_smem(K kernel, int bytes, DeviceOnce& once) {
 template <typename T, int D, int KIND>
 cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
   constexpr bool kTc = sizeof(T) == 2;  // 16-bit queries: the tensor cores
-  p.ctas = kTc ? seq_tc_ctas(D, KIND == SEQ_KV8, device_sms()) : std::min(3 * device_sms(), kSeqMaxCtas);
+  const int ctas = kTc ? seq_tc_ctas(D, p.G, KIND == SEQ_KV8, device_sms()) : std::min(3 * device_sms(), kSeqMaxCtas);
+  p.teams = std::max(1, ctas / p.items);
+  p.ctas = p.teams * p.items;
+  // pieces of a row: the prefix's, and its share of the teams; a warp for every four
+  const int pieces = p.splits + p.teams / p.B + 1;
+  p.merge_warps = pieces <= 4 ? 1 : pieces <= 8 ? 2 : pieces <= 16 ? 4 : 8;
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv;
-  seq_prep_kernel<T, D, KIND>
-      <<<static_cast<unsigned>(1 + (rows + kPrepWarps - 1) / kPrepWarps), kPrepThreads, 0, st>>>(p);
   int launches = 1;
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (p.block == 0) {
+    const int64_t jobs = rows * (KIND == SEQ_KV8 && kTc ? 2 + p.G : 2);
+    seq_prep_kernel<T, D, KIND>
+        <<<static_cast<unsigned>(1 + (jobs + kPrepWarps - 1) / kPrepWarps), kPrepThreads, 0, st>>>(p);
+    e = cudaGetLastError();
+  } else if constexpr (KIND == SEQ_PLAIN) {
+    const int64_t chunks = cdiv(p.n_blocks, kScoreBlocks);
+    block_score_kernel<T, D><<<static_cast<unsigned>(1 + rows * chunks), kScoreThreads, 0, st>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess)
+      e = launch_after(block_select_kernel, dim3(static_cast<unsigned>(rows)), dim3(kSelThreads), 0, st, p);
+    ++launches;
+  }
   if constexpr (KIND == SEQ_PLAIN) {
-    if (e == cudaSuccess && p.block) {
-      const dim3 grid(cdiv(p.n_blocks, kScoreBlocks), static_cast<unsigned>(rows));
-      e = launch_after(block_score_kernel<T, D>, grid, dim3(kScoreThreads), 0, st, p);
-      if (e == cudaSuccess)
-        e = launch_after(block_select_kernel, dim3(static_cast<unsigned>(rows)), dim3(kSelThreads), 0, st, p);
-      launches += 2;
-    }
     if (e == cudaSuccess && p.N > 0) {
       if constexpr (kTc) {
         e = launch_prefix_tc(p.q, p.k_prefix, p.v_prefix, p.N, p.B, p.Hq, p.Hkv, D, p.splits, p.scale_log2, p.pre_o,
@@ -783,7 +888,8 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
   }
   if (e == cudaSuccess) {
     const int64_t heads = static_cast<int64_t>(p.B) * p.Hq;
-    e = launch_after(seq_merge_kernel<T, D>, dim3(static_cast<unsigned>((heads + 7) / 8)), dim3(256), 0, st, p);
+    const int per = 8 / p.merge_warps;
+    e = launch_after(seq_merge_kernel<T, D>, dim3(static_cast<unsigned>((heads + per - 1) / per)), dim3(256), 0, st, p);
     ++launches;
   }
   count_launches(launches);
@@ -912,7 +1018,8 @@ extern "C" swa_status swa_decode_sparse(const void* q, const void* k_new, const 
   if (const swa_status s = seq_sizes(p, head_dim, dtype)) return s;
   if (!block_size(block)) return SWA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(n_first) + n_last > n_select || n_select > (1 << 20) ||
-      static_cast<int64_t>(B) * Hkv > 65535)
+      static_cast<int64_t>(B) * Hkv > 65535 ||
+      static_cast<int64_t>(B) * Hkv * (W / block / kScoreBlocks + 2) > 0x7fffffffll)
     return SWA_ERR_SHAPE;
   if (B == 0) return SWA_OK;
   if (!bounds || !selected) return SWA_ERR_ARG;

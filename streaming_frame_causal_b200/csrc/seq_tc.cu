@@ -49,6 +49,9 @@ namespace {
 constexpr int kThreads = 192;
 constexpr int kN = kSeqCols;  // columns of S^T
 
+#ifndef SWA_SEQ_CTAS8
+#define SWA_SEQ_CTAS8 4
+#endif
 template <int D, int GP, bool KV8>
 struct SeqTcPlan {
   static constexpr int kElem = KV8 ? 1 : 2;
@@ -56,30 +59,29 @@ struct SeqTcPlan {
   static constexpr int kSubBytesRow = kRowBytes < 128 ? kRowBytes : 128;  // of a swizzled sub-tile
   static constexpr int kSubs = kRowBytes / kSubBytesRow;
   static constexpr int kSub = kSeqKeys * kSubBytesRow;
-  static constexpr int kTile = kSubs * kSub;
-  static constexpr int kStage = 2 * kTile;
-  // CTAs per SM: the softmax of a tile is a chain of latencies (TMEM load, exchange
-  // between the warps, hand-off), which two CTAs overlap where 96 KB of ring are deep
-  // enough; a 16-bit tile at head_dim 128 fills 64 KB, and the SM's memory takes one CTA
-  static constexpr int kPerSm = kStage <= 32 * 1024 ? 2 : 1;
-  static constexpr int kStages = (kPerSm == 2 ? 96 : 192) * 1024 / kStage;
-  static constexpr int kON = KV8 && GP == 8 ? 32 : 16;                // columns of O^T
-  static constexpr int kQSub = kN * kSubBytesRow;
+  static constexpr int kUnit = kSubs * kSub;                          // a K or a V tile
+  static constexpr int kPerSm = kUnit > 16 * 1024 ? 2 : (GP == 8 ? 3 : (KV8 ? SWA_SEQ_CTAS8 : 4));
+  static constexpr int kUnits = (kUnit > 16 * 1024 ? 96 : (kPerSm == 4 ? 48 : (KV8 ? 56 : 64))) * 1024 / kUnit;
+  static constexpr int kOCols = (KV8 ? 3 : 1) * GP;                   // columns of O^T that count
+  static constexpr int kON = kOCols > 16 ? 32 : 16;
+  // The products take 16 (or 32) rows of Q and P^T; those behind the ones that count are
+  // whatever follows in shared memory and end in columns that are never read.
+  static constexpr int kQRows = (KV8 ? 2 : 1) * GP > 8 ? 16 : 8;
+  static constexpr int kQSub = kQRows * kSubBytesRow;
   static constexpr int kQ = kSubs * kQSub;
-  static constexpr int kPSub = kN * 128;
-  static constexpr int kP = KV8 ? kON * 128 : 2 * kPSub;  // rows of 128 bytes; 16-bit: of two 128-byte halves
-  // a stage holds V, then K: at head_dim 64 the second product reads 64 rows of M past
-  // its V tile (rows D..127 of O^T, never read), which is then the K tile beside it
-  static constexpr int kOffK = kTile;
-  static constexpr int kOffQ = kStages * kStage;
-  static constexpr int kOffP = kOffQ + 2 * kQ;
-  static constexpr int kOffRed = kOffP + 2 * kP;  // [2][4][8] tile maxima, [4][8] row sums
+  static constexpr int kPSub = (kOCols + 7) / 8 * 1024;               // rows of 128 bytes
+  static constexpr int kP = KV8 ? kPSub : 2 * kPSub;                  // 16-bit: two halves of the keys
+  static constexpr int kOffP = (kUnits * kUnit + 1023) / 1024 * 1024;
+  static constexpr int kOffQ = kOffP + 2 * kP;
+  static constexpr int kOffRed = kOffQ + 2 * kQ;  // [2][4][8] tile maxima, [4][8] row sums
   static constexpr int kOffBar = kOffRed + 3 * 4 * kSeqRows * 4;
-  static constexpr int kNumBars = 2 + 2 + 2 * kStages + 2 + 2 + 2 + 4;
+  static constexpr int kNumBars = 2 + 2 + 2 * kUnits + 2 + 2 + 2 + 4;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
-  static constexpr int kSmem = kOffTmem + 16 + 1024;  // + alignment slack
+  static constexpr int kReadEnd = kOffQ + kQ + (kSubs - 1) * kQSub + kN * kSubBytesRow;
+  static constexpr int kBytes = kOffTmem + 16 > kReadEnd ? kOffTmem + 16 : kReadEnd;
+  static constexpr int kSmem = kBytes + 1024;  // + alignment slack
   static_assert((kSmem + 1024) * kPerSm <= 228 * 1024, "shared memory");
-  static_assert(kQ % 1024 == 0 && kP % 1024 == 0, "swizzle atoms");
+  static_assert(kUnit % 1024 == 0 && kP % 1024 == 0 && kQSub % 512 == 0, "swizzle atoms");
   static constexpr uint32_t kTmemCols = 64;  // S^T 2 x 16 | O^T 16 or 32
   static constexpr float kGrow = KV8 ? 4.f : 8.f;
 };
@@ -160,7 +162,7 @@ template <int D, int GP, bool KV8>
 __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     seq_tc_kernel(const __grid_constant__ SeqTcParams tp) {
   using PL = SeqTcPlan<D, GP, KV8>;
-  constexpr int kStages = PL::kStages;
+  constexpr int kUnits = PL::kUnits;
   const SeqParams& p = tp.s;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
@@ -174,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
   auto q_full = [&](int i) { return bar0 + 8u * i; };
   auto q_free = [&](int i) { return bar0 + 8u * (2 + i); };
   auto kv_full = [&](int s) { return bar0 + 8u * (4 + s); };
-  auto kv_empty = [&](int s) { return bar0 + 8u * (4 + kStages + s); };
-  constexpr int kB = 4 + 2 * kStages;
+  auto kv_empty = [&](int s) { return bar0 + 8u * (4 + kUnits + s); };
+  constexpr int kB = 4 + 2 * kUnits;
   auto s_full = [&](int i) { return bar0 + 8u * (kB + i); };
   auto p_full = [&](int i) { return bar0 + 8u * (kB + 2 + i); };
   auto p_free = [&](int i) { return bar0 + 8u * (kB + 4 + i); };
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       mbar_init(p_full(i), 128);
       mbar_init(p_free(i), 1);
     }
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kUnits; ++s) {
       mbar_init(kv_full(s), 1);
       mbar_init(kv_empty(s), 1);
     }
@@ -215,10 +217,15 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
   SeqWalk walk;
   walk.start(p, blockIdx.x);
   SeqRun run;
+  // The ring's units are K and V tiles in the order the products take them:
+  // K_0, K_1 V_0, K_2 V_1, ..., V_last (tile j of the CTA's share).
+  const int last = walk.left - 1;
+  auto k_unit = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
+  auto v_unit = [&](int j) { return j == last ? 2 * j + 1 : 2 * j + 2; };
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    // the lanes issue the boxes of a tile side by side: one box of 128 rows per sub-tile
-    // of K and of V, or one per selected block (8 of them at most, 32 pieces)
+    // the lanes issue the boxes of a tile side by side: one box of 128 rows per sub-tile,
+    // or one per selected block (8 of them at most, 16 pieces)
     if (lane == 0) {
       tma_prefetch_desc(&tp.tm_k);
       tma_prefetch_desc(&tp.tm_v);
@@ -226,48 +233,56 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     }
     const int rows = p.block ? p.block : kSeqKeys;  // of a box
     const int per_tile = kSeqKeys / rows;
-    int lu = 0, jj = 0;
+    const int box = lane / PL::kSubs, sub = lane % PL::kSubs;
+    const uint32_t dst = base + sub * PL::kSub + box * rows * PL::kSubBytesRow;
+    int lu = 0, jj = 0, unit = 0;
     bool ok = true;
-    while (ok && walk.next(p, blockIdx.x, run)) {
+    // the next unit of the ring: a tile of ``boxes`` boxes, this lane's from ``row`` on (-1: none)
+    auto load = [&](const CUtensorMap* tm, int b, int kvh, int boxes, int row) -> bool {
+      const int u = unit % kUnits;
+      if (unit >= kUnits &&
+          !__all_sync(0xffffffffu, mbar_wait(kv_empty(u), ((unit / kUnits) - 1) & 1, p.err, ERR_WAIT_TMA)))
+        return false;
+      if (lane == 0) mbar_arrive_expect_tx(kv_full(u), boxes * rows * PL::kRowBytes);
+      __syncwarp();
+      if (row >= 0) tma_load_4d(dst + u * PL::kUnit, tm, kv_full(u), sub * 64, kvh, row, b);
+      ++unit;
+      return true;
+    };
+    int b1 = 0, h1 = 0, boxes1 = 0, row1 = 0;  // the tile whose V comes next
+    while (ok && walk.next(p, run)) {
       const int qb = lu & 1;
       if (lu >= 2 &&
           !__all_sync(0xffffffffu, mbar_wait(q_free(qb), ((lu >> 1) - 1) & 1, p.err, ERR_WAIT_TMA))) {
         ok = false;
         break;
       }
-      const int kvh = run.item;
+      const int kvh = walk.item;
       if (lane == 0) {
         mbar_arrive_expect_tx(q_full(qb), PL::kQ);
-        for (int sub = 0; sub < PL::kSubs; ++sub)
-          tma_2d(base + PL::kOffQ + qb * PL::kQ + sub * PL::kQSub, &tp.tm_q, q_full(qb), sub * 64,
+        for (int i = 0; i < PL::kSubs; ++i)
+          tma_2d(base + PL::kOffQ + qb * PL::kQ + i * PL::kQSub, &tp.tm_q, q_full(qb), i * 64,
                  KV8 ? (run.b * p.Hkv + kvh) * kN : run.b * p.Hq + kvh * p.G);
       }
       ++lu;
       const int* sel = p.block ? p.selected + (static_cast<int64_t>(run.b) * p.Hkv + kvh) * p.n_select : nullptr;
       const int n_blocks = p.block ? min((seq_tokens(p, run.b) + p.block - 1) / p.block, p.n_select) : 0;
-      for (int j = 0; j < run.tiles; ++j, ++jj) {
-        const int st = jj % kStages;
+      for (int j = 0; j < run.tiles && ok; ++j, ++jj) {
         const int first = (run.t0 + j) * per_tile;  // box of the item
         const int boxes = p.block ? min(per_tile, n_blocks - first) : 1;
-        // this lane's piece: of box lane / (2 kSubs), K or V, sub-tile
-        const int box = lane / (2 * PL::kSubs), piece = lane % (2 * PL::kSubs);
-        const int kv = piece / PL::kSubs, sub = piece % PL::kSubs;
         const int row = box >= boxes ? -1 : (p.block ? sel[first + box] * p.block : first * kSeqKeys);
-        if (jj >= kStages && !__all_sync(0xffffffffu, mbar_wait(kv_empty(st), ((jj / kStages) - 1) & 1, p.err,
-                                                                 ERR_WAIT_TMA))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(kv_full(st), 2 * boxes * rows * PL::kRowBytes);
-        __syncwarp();
-        if (row >= 0)
-          tma_load_4d(base + st * PL::kStage + (kv ? 0 : PL::kOffK) + sub * PL::kSub + box * rows * PL::kSubBytesRow,
-                      kv ? &tp.tm_v : &tp.tm_k, kv_full(st), sub * 64, kvh, row, run.b);
+        ok = load(&tp.tm_k, run.b, kvh, boxes, row);
+        if (ok && jj > 0) ok = load(&tp.tm_v, b1, h1, boxes1, row1);
+        b1 = run.b;
+        h1 = kvh;
+        boxes1 = boxes;
+        row1 = row;
       }
     }
+    if (ok && jj > 0) load(&tp.tm_v, b1, h1, boxes1, row1);
     // never leave with a bulk copy still landing in shared memory
-    for (int j = jj - kStages; j < jj; ++j)
-      if (j >= 0) mbar_wait(kv_full(j % kStages), (j / kStages) & 1, p.err, ERR_WAIT_TMA);
+    for (int u = unit - kUnits; u < unit; ++u)
+      if (u >= 0) mbar_wait(kv_full(u % kUnits), (u / kUnits) & 1, p.err, ERR_WAIT_TMA);
     for (int i = lu - 2; i < lu; ++i)
       if (i >= 0) mbar_wait(q_full(i & 1), (i >> 1) & 1, p.err, ERR_WAIT_TMA);
   } else if (warp == 1) {
@@ -277,13 +292,14 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, ERR_WAIT_MMA));
     };
-    const uint64_t dk0 = sdesc_rows<PL::kSubBytesRow>(base + PL::kOffK, 16);  // K of stage 0 (A, K-major)
-    // V of stage 0 (A, MN-major): groups of M rows are sub-tiles apart
-    const uint64_t dv0 = sdesc_rows<PL::kSubBytesRow>(base, PL::kSub);
+    const uint64_t dk0 = sdesc_rows<PL::kSubBytesRow>(base, 16);  // K in unit 0 (A, K-major)
+    // V in unit 0 (A, MN-major): groups of M rows are sub-tiles apart; at head_dim 64 there
+    // is one, and the second half of M repeats it (rows D..127 of O^T, never read)
+    const uint64_t dv0 = sdesc_rows<PL::kSubBytesRow>(base, D == 64 ? 0 : PL::kSub);
     const uint64_t dq0 = sdesc_rows<PL::kSubBytesRow>(base + PL::kOffQ, 16);  // (B, K-major)
     const uint64_t dp0 = sdesc_rows<128>(base + PL::kOffP, 16);               // (B, K-major)
     auto issue_s = [&](int jj, int qb) {
-      const uint64_t dk = dk0 + (jj % kStages) * static_cast<uint64_t>(PL::kStage >> 4);
+      const uint64_t dk = dk0 + (k_unit(jj) % kUnits) * static_cast<uint64_t>(PL::kUnit >> 4);
       const uint64_t dq = dq0 + qb * static_cast<uint64_t>(PL::kQ >> 4);
       const uint32_t tS = tm + (jj & 1) * kN;
 #pragma unroll
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       }
     };
     auto issue_o = [&](int jj, bool acc) {
-      const uint64_t dv = dv0 + (jj % kStages) * static_cast<uint64_t>(PL::kStage >> 4);
+      const uint64_t dv = dv0 + (v_unit(jj) % kUnits) * static_cast<uint64_t>(PL::kUnit >> 4);
       const uint64_t dp = dp0 + (jj & 1) * static_cast<uint64_t>(PL::kP >> 4);
       const uint32_t tO = tm + 2 * kN;
       constexpr int kKeys = 32 / PL::kElem;  // keys of an instruction
@@ -315,16 +331,17 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     int prev = -1;  // tile whose second product is pending
     bool prev_first = false, prev_last = false, ok = true;
     auto finish_prev = [&]() -> bool {
-      if (!wait(p_full(prev & 1), (prev >> 1) & 1)) return false;
+      const int u = v_unit(prev);
+      if (!wait(kv_full(u % kUnits), (u / kUnits) & 1) || !wait(p_full(prev & 1), (prev >> 1) & 1)) return false;
       tc_fence_after();
       issue_o(prev, !prev_first);
-      mma_commit_if(issue, kv_empty(prev % kStages));
+      mma_commit_if(issue, kv_empty(u % kUnits));
       mma_commit_if(issue, p_free(prev & 1));
       mma_commit_if(issue, o_done);
       if (prev_last) mma_commit_if(issue, o_full);
       return true;
     };
-    while (ok && walk.next(p, blockIdx.x, run)) {
+    while (ok && walk.next(p, run)) {
       const int qb = lu & 1;
       if (!wait(q_full(qb), (lu >> 1) & 1)) {
         ok = false;
@@ -332,13 +349,15 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       }
       ++lu;
       for (int j = 0; j < run.tiles; ++j, ++jj) {
-        if (!wait(kv_full(jj % kStages), (jj / kStages) & 1)) {
+        const int u = k_unit(jj);
+        if (!wait(kv_full(u % kUnits), (u / kUnits) & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
         issue_s(jj, qb);
         mma_commit_if(issue, s_full(jj & 1));
+        mma_commit_if(issue, kv_empty(u % kUnits));
         if (j == run.tiles - 1) mma_commit_if(issue, q_free(qb));
         if (prev >= 0 && !finish_prev()) {
           ok = false;
@@ -370,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, ERR_WAIT_SOFTMAX));
     };
-    while (ok && walk.next(p, blockIdx.x, run)) {
-      const int kvh = run.item, b = run.b;
+    while (ok && walk.next(p, run)) {
+      const int kvh = walk.item, b = run.b;
       const int64_t qrow = static_cast<int64_t>(b) * p.Hq + kvh * p.G;
       const int n_tokens = seq_tokens(p, b);
       const int64_t ebase = (static_cast<int64_t>(b) * p.Hkv + kvh) * p.W;
@@ -412,14 +431,21 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
         tmem_ld16(tmem + lane_off + sb * kN, sv);
         tmem_wait_ld();
         if (!valid) {
-          // The key's V row in the tile is whatever the slot or the stage held.  Its weight
-          // is 0, but 0 x NaN is NaN, so the row is zeroed before the second product
-          // reads it (the proxy fence before the p_full arrival orders these stores first).
-          const uint32_t vrow = base + (jj % kStages) * PL::kStage + r * PL::kSubBytesRow;
+          // The key's V row in the tile is whatever the slot or the unit held.  Its weight
+          // is 0, but 0 x NaN is NaN, so the row is zeroed, once V has landed, before the
+          // second product reads it (the proxy fence before the p_full arrival orders
+          // these stores first).
+          const int u = v_unit(jj);
+          if (!mbar_wait(kv_full(u % kUnits), (u / kUnits) & 1, p.err, ERR_WAIT_SOFTMAX)) ok = false;
+          const uint32_t vrow = base + (u % kUnits) * PL::kUnit + r * PL::kSubBytesRow;
 #pragma unroll
           for (int sub = 0; sub < PL::kSubs; ++sub)
 #pragma unroll
             for (int o = 0; o < PL::kSubBytesRow; o += 16) st_zero16(vrow + sub * PL::kSub + o);
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
         }
         float x[GP];
         const float kscale = KV8 ? __uint_as_float(static_cast<uint32_t>(ke0) << 23) : 1.f;
@@ -618,12 +644,19 @@ cudaError_t launch_d(const SeqTcParams& p, cudaStream_t st) {
 
 }  // namespace
 
-int seq_tc_ctas(int D, bool kv8, int sms) {
-  const bool two = kv8 || D == 64;
-  static_assert(SeqTcPlan<128, 8, true>::kPerSm == 2 && SeqTcPlan<64, 8, true>::kPerSm == 2 &&
-                    SeqTcPlan<64, 8, false>::kPerSm == 2 && SeqTcPlan<128, 8, false>::kPerSm == 1,
-                "CTAs per SM");
-  return std::min(two ? 2 * sms : sms, kSeqMaxCtas);
+template <int D, bool KV8>
+int ctas_per_sm(int columns) {
+  return columns == 8   ? SeqTcPlan<D, 8, KV8>::kPerSm
+         : columns == 4 ? SeqTcPlan<D, 4, KV8>::kPerSm
+         : columns == 2 ? SeqTcPlan<D, 2, KV8>::kPerSm
+                        : SeqTcPlan<D, 1, KV8>::kPerSm;
+}
+
+int seq_tc_ctas(int D, int G, bool kv8, int sms) {
+  const int c = seq_head_columns(G);
+  const int per_sm = D == 64 ? (kv8 ? ctas_per_sm<64, true>(c) : ctas_per_sm<64, false>(c))
+                             : (kv8 ? ctas_per_sm<128, true>(c) : ctas_per_sm<128, false>(c));
+  return std::min(per_sm * sms, kSeqMaxCtas);
 }
 
 cudaError_t launch_seq_tc(const SeqParams& s, int D, bool kv8, cudaStream_t st) {
@@ -639,7 +672,7 @@ cudaError_t launch_seq_tc(const SeqParams& s, int D, bool kv8, cudaStream_t st) 
   const uint64_t qdims[2] = {static_cast<uint64_t>(D),
                              kv8 ? static_cast<uint64_t>(s.B) * s.Hkv * kN : static_cast<uint64_t>(s.B) * s.Hq};
   const uint64_t qstride[1] = {D * e};
-  const uint32_t qbox[2] = {cols, kN};
+  const uint32_t qbox[2] = {cols, (kv8 ? 2u : 1u) * seq_head_columns(s.G) > 8 ? 16u : 8u};
   const int swizzle = static_cast<int>(cols * e);
   if (!encode_tiled(&p.tm_k, static_cast<int>(e), s.k_cache, 4, dims, strides, box, swizzle) ||
       !encode_tiled(&p.tm_v, static_cast<int>(e), s.v_cache, 4, dims, strides, box, swizzle) ||
