@@ -2,10 +2,11 @@
 // they are written (swa_kv8_write) and read back (swa_kv8_read).  The format is
 // kv8.cuh's.
 //
-// Bound: device memory.  A row of D elements belongs to D / 8 neighbouring lanes,
-// eight elements each (16 bytes in, 8 out at 16 bits), whose largest magnitude is a
-// few shuffles; nothing is kept between rows.  The cache's slots are the rolling
-// ones, position mod W, so a run may wrap around its end.
+// Bound: device memory.  A row of D elements belongs to D / 16 neighbouring lanes,
+// 16 elements each (16 bytes of the cache), whose largest magnitude is a few
+// shuffles; a thread loads its part of kRunRows rows before it works on the
+// first.  The cache's slots are the rolling ones, position mod W, so a run may wrap
+// around its end.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -33,53 +34,123 @@ SWA_DEV int run_length(const RunParams& p, int b) {
   return p.count ? min(max(p.count[b], 0), p.T) : p.T;
 }
 
-// grid: x over rows of one sequence (token, head), y the sequence, z K or V
+constexpr int kRunRows = 4;  // rows of a thread
+
+// 16 elements as they are stored
+template <typename T>
+struct Raw16 {
+  static constexpr int kWords = sizeof(T);
+  uint4 w[kWords];
+  SWA_DEV void load(const T* x) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(x)[i];
+  }
+  SWA_DEV void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  SWA_DEV void widen(float* v) const {
+    const T* x = reinterpret_cast<const T*>(w);
+    load8(x, v);
+    load8(x + 8, v + 8);
+  }
+};
+
+// The rows (token, head) of a thread in one sequence's run: r0, r0 + step, ...
+template <int D>
+struct RunRows {
+  static constexpr int kLanes = D / 16;
+  static constexpr int kStep = kRunThreads / kLanes;
+  int64_t r0;
+  int part;
+  SWA_DEV RunRows()
+      : r0(static_cast<int64_t>(blockIdx.x) * (kStep * kRunRows) + threadIdx.x / kLanes), part(threadIdx.x % kLanes) {}
+};
+
+// grid: x over the rows of one sequence, y the sequence, z K or V
 template <typename T, int D>
 __global__ void __launch_bounds__(kRunThreads) kv8_write_kernel(const __grid_constant__ RunParams p) {
-  constexpr int kLanes = D / 8;
-  const int b = blockIdx.y, kv = blockIdx.z;
+  using R = RunRows<D>;
+  const R at;
+  const int b = blockIdx.y;
+  const bool is_v = blockIdx.z;
   const long long pos = p.pos[b];
   const int n = run_length(p, b);
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kRunThreads / kLanes) + threadIdx.x / kLanes;
-  const int t = static_cast<int>(r / p.Hkv), h = static_cast<int>(r - static_cast<int64_t>(t) * p.Hkv);
-  const int part = threadIdx.x % kLanes;
-  // of a run longer than the window only the last W tokens stay
-  const bool live = pos >= 0 && t < n && t >= n - p.W;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live)
-    load8(static_cast<const T*>(p.x[kv]) + ((static_cast<int64_t>(b) * p.T + t) * p.Hkv + h) * D + part * 8, v);
-  float a = amax8(v);
+  if (pos < 0 || (at.r0 - threadIdx.x / R::kLanes) >= static_cast<int64_t>(n) * p.Hkv) return;
+  const T* x = static_cast<const T*>(is_v ? p.x[1] : p.x[0]) + static_cast<int64_t>(b) * p.T * p.Hkv * D + at.part * 16;
+  Raw16<T> raw[kRunRows];
+  bool live[kRunRows];
 #pragma unroll
-  for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-  if (!live) return;
-  const int e = kv8_exponent(a);
-  const int64_t slot = (pos + t) % p.W;
-  *reinterpret_cast<uint2*>(p.x8[kv] + ((static_cast<int64_t>(b) * p.W + slot) * p.Hkv + h) * D + part * 8) =
-      quantise8(v, e);
-  if (part == 0)
-    p.exp[kv][(static_cast<int64_t>(b) * p.Hkv + h) * p.W + slot] = static_cast<uint8_t>(e + 127);
+  for (int i = 0; i < kRunRows; ++i) {
+    const int64_t r = at.r0 + i * R::kStep;
+    // of a run longer than the window only the last W tokens stay
+    live[i] = r < static_cast<int64_t>(n) * p.Hkv && r >= static_cast<int64_t>(n - p.W) * p.Hkv;
+    if (live[i]) raw[i].load(x + r * D);
+    else raw[i].clear();
+  }
+  uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * 16;
+  uint8_t* exps = (is_v ? p.exp[1] : p.exp[0]) + static_cast<int64_t>(b) * p.Hkv * p.W;
+  const int slot0 = static_cast<int>(pos % p.W);
+#pragma unroll
+  for (int i = 0; i < kRunRows; ++i) {
+    float v[16];
+    raw[i].widen(v);
+    float a = fmaxf(amax8(v), amax8(v + 8));
+#pragma unroll
+    for (int off = R::kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    if (live[i]) {
+      const int64_t r = at.r0 + i * R::kStep;
+      const int t = static_cast<int>(r / p.Hkv), h = static_cast<int>(r - static_cast<int64_t>(t) * p.Hkv);
+      const int64_t slot = (static_cast<int64_t>(slot0) + t) % p.W;
+      const int e = kv8_exponent(a);
+      const uint2 lo = quantise8(v, e), hi = quantise8(v + 8, e);
+      *reinterpret_cast<uint4*>(x8 + (slot * p.Hkv + h) * D) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      if (at.part == 0) exps[h * static_cast<int64_t>(p.W) + slot] = static_cast<uint8_t>(e + 127);
+    }
+  }
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kRunThreads) kv8_read_kernel(const __grid_constant__ RunParams p) {
-  constexpr int kLanes = D / 8;
-  const int b = blockIdx.y, kv = blockIdx.z;
+  using R = RunRows<D>;
+  const R at;
+  const int b = blockIdx.y;
+  const bool is_v = blockIdx.z;
   const long long pos = p.pos[b];
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (kRunThreads / kLanes) + threadIdx.x / kLanes;
-  const int t = static_cast<int>(r / p.Hkv), h = static_cast<int>(r - static_cast<int64_t>(t) * p.Hkv);
-  const int part = threadIdx.x % kLanes;
-  if (pos < 0 || t >= run_length(p, b)) return;
-  const int64_t slot = (pos + t) % p.W;
-  const uint2 q = *reinterpret_cast<const uint2*>(
-      p.x8[kv] + ((static_cast<int64_t>(b) * p.W + slot) * p.Hkv + h) * D + part * 8);
-  float v[8];
-  dequantise8(q, p.exp[kv][(static_cast<int64_t>(b) * p.Hkv + h) * p.W + slot] - 127, v);
-  store8(static_cast<T*>(p.x[kv]) + ((static_cast<int64_t>(b) * p.T + t) * p.Hkv + h) * D + part * 8, v);
+  const int64_t rows = static_cast<int64_t>(run_length(p, b)) * p.Hkv;
+  if (pos < 0) return;
+  const uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * 16;
+  const uint8_t* exps = (is_v ? p.exp[1] : p.exp[0]) + static_cast<int64_t>(b) * p.Hkv * p.W;
+  const int slot0 = static_cast<int>(pos % p.W);
+  uint4 q[kRunRows];
+  int e[kRunRows];
+#pragma unroll
+  for (int i = 0; i < kRunRows; ++i) {
+    const int64_t r = at.r0 + i * R::kStep;
+    if (r < rows) {
+      const int t = static_cast<int>(r / p.Hkv), h = static_cast<int>(r - static_cast<int64_t>(t) * p.Hkv);
+      const int64_t slot = (static_cast<int64_t>(slot0) + t) % p.W;
+      q[i] = *reinterpret_cast<const uint4*>(x8 + (slot * p.Hkv + h) * D);
+      e[i] = exps[h * static_cast<int64_t>(p.W) + slot] - 127;
+    }
+  }
+  T* x = static_cast<T*>(is_v ? p.x[1] : p.x[0]) + static_cast<int64_t>(b) * p.T * p.Hkv * D + at.part * 16;
+#pragma unroll
+  for (int i = 0; i < kRunRows; ++i) {
+    const int64_t r = at.r0 + i * R::kStep;
+    if (r < rows) {
+      float v[8];
+      dequantise8(make_uint2(q[i].x, q[i].y), e[i], v);
+      store8(x + r * D, v);
+      dequantise8(make_uint2(q[i].z, q[i].w), e[i], v);
+      store8(x + r * D + 8, v);
+    }
+  }
 }
 
 template <bool kWrite, typename T, int D>
 cudaError_t launch_run(const RunParams& p, cudaStream_t st) {
-  constexpr int kRows = kRunThreads / (D / 8);
+  constexpr int kRows = RunRows<D>::kStep * kRunRows;
   const int64_t rows = static_cast<int64_t>(p.T) * p.Hkv;
   const dim3 grid(static_cast<unsigned>((rows + kRows - 1) / kRows), p.B, 2);
   if (kWrite)

@@ -11,8 +11,8 @@
 // threads, forms their sines and cosines once in shared memory, and every thread
 // then rotates 16-byte pieces of the rows.  The first pieces are loaded before
 // the sines are formed, so that the loads are in flight meanwhile.  Angles are
-// formed and reduced to [-pi, pi] in 64 bits (a position of 10^6 times a rate of 1
-// has no fraction left in 32), the sine and cosine are taken in 32.
+// formed in turns and reduced to half a turn in 64 bits (a position of 10^6 times
+// a rate of 1 has no fraction left in 32), the sine and cosine are taken in 32.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -46,7 +46,7 @@ struct RopeParams {
   int tokens_per_block;
   int inverse;
   int first[kRopeMaxAxes];  // first pair of each axis
-  double rate[kRopeMaxPairs];
+  double rate[kRopeMaxPairs];  // turns per position
 };
 
 // one 16-byte piece: E elements, E / 2 pairs, their (cos, sin) from t on
@@ -105,10 +105,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_nd_kernel(const __grid_cons
     if (j < p.pairs) {
       int a = 0;
       while (a + 1 < p.axes && j >= p.first[a + 1]) ++a;
-      constexpr double kTwoPi = 6.283185307179586476925, kInvTwoPi = 0.15915494309189533576889;
-      const double ang = static_cast<double>(__ldg(p.pos + (tok0 + tk) * p.axes + a)) * p.rate[j];
-      const float r = static_cast<float>(fma(-rint(ang * kInvTwoPi), kTwoPi, ang));
-      sincosf(r, &cs.y, &cs.x);
+      const double turns = static_cast<double>(__ldg(p.pos + (tok0 + tk) * p.axes + a)) * p.rate[j];
+      sincospif(2.f * static_cast<float>(turns - rint(turns)), &cs.y, &cs.x);
       if (p.inverse) cs.y = -cs.y;
     }
     table[i] = cs;
@@ -152,7 +150,7 @@ extern "C" swa_status swa_rope_nd(const void* x, void* y, const int32_t* pos, lo
   for (int a = 0; a < axes; ++a) {
     if (pairs[a] < 0 || pairs[a] > head_dim / 2 - n) return SWA_ERR_SHAPE;
     p.first[a] = n;
-    for (int j = 0; j < pairs[a]; ++j) p.rate[n++] = std::pow(theta, -static_cast<double>(j) / pairs[a]);
+    for (int j = 0; j < pairs[a]; ++j) p.rate[n++] = std::pow(theta, -static_cast<double>(j) / pairs[a]) * 0.15915494309189533576889;
   }
   if (tokens == 0) return SWA_OK;
   if (!x || !y || !pos) return SWA_ERR_ARG;

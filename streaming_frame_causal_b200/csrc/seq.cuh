@@ -4,16 +4,18 @@
 // Every sequence b has its own position pos[b] (in device memory, so that a
 // captured step can be replayed as the positions advance) and so its own number
 // of keys, cut into tiles of 128.  An item is one (sequence, KV head, group of up to 8
-// of its query heads).  The tiles of all sequences, in order, form one line of T, and
-// team c of C takes the tiles [c T / C, (c + 1) T / C): the shares differ by one tile at
-// most, whatever the lengths.  A team is one CTA per item of a sequence, and its
-// CTAs walk the same tiles side by side: a token's KV heads lie next to one another
-// in a cache, so the team reads whole rows of memory together.  (Shares of a line of
-// the items' tiles, with the heads' CTAs at different places, ran the 8-bit decode of 64
-// x 4096 tokens x 8 heads in 128 us against 97.)  A CTA that holds an item whole
-// writes its output; an item cut between teams leaves partial results, two slots
-// per CTA at most (the sequence that runs into its share, and the one that runs out of
-// it), which a second kernel merges in the order of the tiles.
+// of its query heads).  The tiles of all sequences, in order, form one line, in
+// which every sequence begins with kSeqStart tiles' worth of nothing (what changing
+// over to it costs); team c of C takes the part [c T / C, (c + 1) T / C) of its T places.
+// A team is one CTA per item of a sequence, and its CTAs walk the same tiles side by
+// side: a token's KV heads lie next to one another in a cache, so the team reads
+// whole rows of memory together.  (With the heads' CTAs at different places of the
+// line, the 8-bit decode of 64 x 4096 tokens x 8 heads took 128 us against 104.)
+//
+// A CTA that holds an item whole writes its output.  An item cut between teams leaves a
+// partial result in each, at most two per CTA (the sequence that runs into its part, and
+// the one that runs out of it).  A CTA counts them when it has finished, and the last
+// one of an item merges its pieces, in the order of the tiles.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -26,7 +28,8 @@ namespace swa {
 
 constexpr int kSeqKeys = 128;     // keys of a tile
 constexpr int kSeqRows = 8;       // query heads of an item
-constexpr int kSeqMaxCtas = 640;  // CTAs that the workspace has partial slots for (or one team, if that is more)
+constexpr int kSeqMaxCtas = 640;  // CTAs of a launch (or one team, if that is more)
+constexpr int kSeqStart = 2;      // of 0, 1 and 2, 2 ran 33 sequences of 82 to 8192 tokens fastest (43.9, 42.8, 41.3 us)
 constexpr int kSeqCols = 16;      // query columns of the tensor-core products
 constexpr int kSeqMaxSplits = 64; // pieces of a shared prefix
 
@@ -45,10 +48,11 @@ struct SeqParams {
   uint64_t* score;        // [B * Hkv, blocks] sortable
   const void* k_prefix;   // [N, Hkv, D]
   const void* v_prefix;
-  int* cum;               // [B + 1] tiles of the sequences, summed
   int4* share;            // [teams] {sequence, first tile of it, tiles}
-  float* part_o;          // [slots, 8, D]
-  float* part_ml;         // [slots, 8, 2] maximum in log2 units, sum
+  int2* own;              // [B] {first team that holds tiles of the sequence, teams that do}
+  int* count;             // [B * items] pieces of an item that are done
+  float* part_o;          // [slots, part_rows, D]
+  float* part_ml;         // [slots, part_rows, 2] maximum in log2 units, sum
   float* pre_o;           // [splits, B * Hq, D]
   float* pre_ml;          // [splits, B * Hq, 2]
   uint8_t* q8;            // 8-bit caches: [B * Hkv, 16, D] the queries as two e4m3 terms
@@ -59,6 +63,7 @@ struct SeqParams {
   int block, n_select, n_first, n_last, n_blocks;  // block-sparse (block = 0: all keys)
   int N, splits;          // shared prefix
   int teams, ctas;        // ctas = teams * items
+  int part_rows;          // min(G, 8)
   int merge_warps;        // warps that merge one row's pieces
   float scale_log2;
 };
@@ -77,19 +82,13 @@ SWA_DEV int seq_tiles(const SeqParams& p, int b) {
   return (blocks * p.block + kSeqKeys - 1) / kSeqKeys;
 }
 
-// teams that share a line of T tiles: no share is empty, so that the pieces of a cut
-// item are those of consecutive teams
-SWA_DEV int seq_teams(const SeqParams& p, int T) { return T < p.teams ? T : p.teams; }
-
-// team that owns tile t of the line of T: the c with c T / C <= t < (c + 1) T / C
-SWA_DEV int seq_owner(int t, int T, int teams) {
-  return static_cast<int>((static_cast<int64_t>(t + 1) * teams - 1) / T);
-}
+// team that owns place t of the line of T >= teams: the c with c T / C <= t < (c + 1) T / C
+SWA_DEV int seq_owner(int64_t t, int64_t T, int teams) { return static_cast<int>(((t + 1) * teams - 1) / T); }
 
 // A run of tiles of one sequence within a CTA's share.
 struct SeqRun {
-  int b, t0, tiles;  // tiles [t0, t0 + tiles) of the CTA's item of sequence b
-  int slot;          // partial slot; -1: the item is whole, its output is written
+  int b, t0, tiles, tokens;  // tiles [t0, t0 + tiles) of the CTA's item of sequence b
+  int slot;                  // partial slot; -1: the item is whole, its output is written
 };
 
 // Walks a CTA's share.  Every role of a CTA walks it for itself.
@@ -114,11 +113,73 @@ struct SeqWalk {
     r.b = b;
     r.t0 = t0;
     r.tiles = min(left, of - t0);
+    r.tokens = seq_tokens(p, b);
     // with a shared prefix every item is merged with the prefix's pieces
     r.slot = r.tiles == of ? (p.N > 0 ? 2 * p.ctas + b * p.items + item : -1) : 2 * cta + (t0 == 0 ? 1 : 0);
     left -= r.tiles;
     t0 = of;
     return true;
+  }
+};
+
+// The pieces o(i) = [D] sums, ml(i) = {maximum, sum} for i < n, merged by a warp: lane
+// ``lane`` returns its D / 32 elements of sum_i 2^(m_i - M) O_i, and L = sum_i 2^(m_i - M) l_i.
+// A lane holds one piece's weight, and the outputs are added with independent loads
+// (from L2: other SMs have just written them).
+template <int D, typename O, typename ML>
+SWA_DEV void merge_pieces(int n, int stride, int first, int lane, O o_of, ML ml_of, float* acc, float& M, float& L) {
+  constexpr int E = D / 32;
+  M = -INFINITY;
+  L = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i0 = first; i0 < n; i0 += 32 * stride) {
+    const int i = i0 + lane * stride;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (i < n) ml = __ldcg(reinterpret_cast<const float2*>(ml_of(i)));
+    float top = ml.x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    top = fmaxf(top, M);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float w = exp2f(ml.x - ref), keep = exp2f(M - ref);
+    float sum = w * ml.y;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    L = L * keep + sum;
+    M = top;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= keep;
+    const int k1 = min(32, (n - i0 + stride - 1) / stride);
+#pragma unroll 4
+    for (int k = 0; k < k1; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* o = o_of(i0 + k * stride) + lane * E;
+      float v[E];
+      if constexpr (E == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(o));
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      } else if constexpr (E == 2) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(o));
+        v[0] = x.x; v[1] = x.y;
+      } else {
+        v[0] = __ldcg(o);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, v[e], acc[e]);
+    }
+  }
+}
+
+// Row ``row`` of the partials of an item of sequence b that ``own`` teams hold.
+struct SeqPieces {
+  const SeqParams& p;
+  int b, item, row;
+  int2 own;
+  SWA_DEV int64_t at(int i) const {
+    const int64_t slot = own.y == 1 ? 2 * p.ctas + static_cast<int64_t>(b) * p.items + item
+                                    : 2 * (static_cast<int64_t>(own.x + i) * p.items + item) + (i == 0 ? 1 : 0);
+    return slot * p.part_rows + row;
   }
 };
 

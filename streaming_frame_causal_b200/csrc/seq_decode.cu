@@ -5,7 +5,7 @@
 // One step is a chain of kernels, each a programmatic dependent launch behind the
 // one before: the new token enters the cache and the work is divided (seq.cuh);
 // block-sparse: scores and selection; the prefix's pieces; the attention over the
-// caches; the merge of what was cut.
+// caches; with a prefix, the merge.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -31,48 +31,85 @@ SWA_DEV void put_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 constexpr int kPrepThreads = 256;
 constexpr int kPrepWarps = kPrepThreads / 32;
 
-// one block: the sequences' tiles summed, and every team's share of their line
-SWA_DEV void seq_divide(const SeqParams& p) {
+// exclusive sum over the block's threads of v, and the total
+SWA_DEV int block_sum(int v, int& total) {
   __shared__ int sums[kPrepWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int carry = 0;
+  int s = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += y;
+  }
+  if (lane == 31) sums[warp] = s;
+  __syncthreads();
+  int before = s - v;
+  total = 0;
+  for (int w = 0; w < kPrepWarps; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  __syncthreads();
+  return before;
+}
+
+// one block: every team's share of the line, and every sequence's teams
+SWA_DEV void seq_divide(const SeqParams& p) {
+  // for now own[b] = {places, tiles} in front of sequence b
+  int T = 0, tiles = 0, n;
   for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
     const int b = b0 + threadIdx.x;
-    const int v = b < p.B ? seq_tiles(p, b) : 0;
-    int s = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, off);
-      if (lane >= off) s += y;
-    }
-    if (lane == 31) sums[warp] = s;
-    __syncthreads();
-    int before = carry;
-    for (int w = 0; w < kPrepWarps; ++w) {
-      if (w < warp) before += sums[w];
-      carry += sums[w];
-    }
-    if (b < p.B) p.cum[b] = before + s - v;
-    __syncthreads();
+    const int mine = b < p.B ? seq_tiles(p, b) : 0;
+    int2 before;
+    before.x = T + block_sum(mine > 0 ? mine + kSeqStart : 0, n);
+    T += n;
+    before.y = tiles + block_sum(mine, n);
+    tiles += n;
+    if (b < p.B) p.own[b] = before;
   }
-  if (threadIdx.x == 0) p.cum[p.B] = carry;
   __syncthreads();
-  const int teams = seq_teams(p, carry);
+  const int teams = min(p.teams, T);  // no part is empty
   for (int c = threadIdx.x; c < p.teams; c += kPrepThreads) {
     int4 s = make_int4(0, 0, 0, 0);
     if (c < teams) {
-      const int t = static_cast<int>(static_cast<int64_t>(carry) * c / teams);
-      const int end = static_cast<int>(static_cast<int64_t>(carry) * (c + 1) / teams);
-      int lo = 0, hi = p.B;  // the last b whose tiles begin at t or before it
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cum[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      s = make_int4(lo, t - p.cum[lo], end - t, 0);
+      // the sequence that holds place t < T, and the tiles in front of t
+      auto find = [&](int t, int& lo) {
+        lo = 0;  // the last b whose places begin at t or before it
+        for (int hi = p.B; hi - lo > 1;) {
+          const int mid = (lo + hi) >> 1;
+          if (p.own[mid].x <= t) lo = mid;
+          else hi = mid;
+        }
+        return p.own[lo].y + max(0, t - p.own[lo].x - kSeqStart);
+      };
+      const int t = static_cast<int>(static_cast<int64_t>(T) * c / teams);
+      const int end = static_cast<int>(static_cast<int64_t>(T) * (c + 1) / teams);
+      int other;
+      const int first = find(t, s.x);
+      s.y = first - p.own[s.x].y;
+      s.z = (end < T ? find(end, other) : tiles) - first;
     }
     p.share[c] = s;
   }
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
+    const int of = seq_tiles(p, b), t = p.own[b].x + kSeqStart;
+    int2 s = make_int2(0, 0);
+    if (of > 0) {
+      s.x = seq_owner(t, T, teams);
+      s.y = seq_owner(t + of - 1, T, teams) - s.x + 1;
+    }
+    p.own[b] = s;
+  }
+}
+
+// One warp: nothing of the items of (sequence, KV head) row is done yet; an idle row's output
+template <typename T, int D>
+SWA_DEV void seq_start_row(const SeqParams& p, int64_t row, bool idle, int lane) {
+  for (int i = lane; i < p.groups; i += 32) p.count[row * p.groups + i] = 0;
+  if (!idle) return;
+  T* out = static_cast<T*>(p.out) + row * p.G * D;
+  for (int i = lane; i < p.G * D; i += 32) put_f32(out + i, 0.f);
 }
 
 // Block 0 divides the work; the warps of the other blocks take a row each: the new
@@ -100,6 +137,7 @@ __global__ void __launch_bounds__(kPrepThreads) seq_prep_kernel(const __grid_con
 #pragma unroll
   for (int i = 0; i < E; ++i) x[i] = src[i];
   const long long pos = p.pos[b];
+  if (what == 0) seq_start_row<T, D>(p, row, pos < 0, lane);
   if (pos < 0) return;
   const int slot = static_cast<int>(pos % p.W);
   const int64_t at = ((static_cast<int64_t>(b) * p.W + slot) * p.Hkv + h) * D + lane * E;
@@ -219,6 +257,39 @@ SWA_DEV void load16(const T* x, float* v) {
   }
 }
 
+// A 32-bit float in 64 bits.  The conversion instruction runs at a quarter of the rate of a
+// 64-bit product, so normal numbers are widened by moving their fields; the rest
+// (zero, subnormal, infinite, NaN) are converted.
+SWA_DEV bool is_normal_bits(uint32_t u) { return (u & 0x7fffffffu) - 0x00800000u < 0x7f000000u; }
+SWA_DEV double widen_bits(uint32_t u) {
+  const uint32_t hi = (((u & 0x7fffffffu) >> 3) + (896u << 20)) | (u & 0x80000000u);
+  return __hiloint2double(static_cast<int>(hi), static_cast<int>(u << 29));
+}
+
+// w . the 16 bytes of a row in v
+template <typename T>
+SWA_DEV double dot_piece(uint4 v, const double* w) {
+  constexpr int E = 16 / sizeof(T);
+  const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+  uint32_t u[E];
+  bool normal = true;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if constexpr (sizeof(T) == 2) u[i] = i & 1 ? word[i / 2] & 0xffff0000u : word[i / 2] << 16;
+    else u[i] = word[i];
+    normal &= is_normal_bits(u[i]);
+  }
+  double s = 0.0;
+  if (normal) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) s = fma(widen_bits(u[i]), w[i], s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) s = fma(static_cast<double>(__uint_as_float(u[i])), w[i], s);
+  }
+  return s;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
@@ -236,6 +307,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
   const int j0 = static_cast<int>(u - row * chunks) * kScoreBlocks;
   const int n = seq_tokens(p, b);
   const int used = n > 0 ? (n + p.block - 1) / p.block : 0;
+  if (j0 == 0 && threadIdx.x < 32) seq_start_row<T, D>(p, row, n == 0, threadIdx.x);
   if (j0 >= used) return;
   const int slot = static_cast<int>(p.pos[b] % p.W), newest = slot / p.block;
   const int part = threadIdx.x % kLanes, r = threadIdx.x / kLanes;
@@ -284,39 +356,50 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     }
     __syncthreads();
   }
+  // the rows of a thread's blocks first, so that they are on their way
+  constexpr int kIter = kScoreBlocks / kRows;
+  constexpr int kAhead = kIter < 4 ? kIter : 4;
+  uint4 lo[kAhead], hi[kAhead];
+  auto load = [&](int i) {
+    const int j = j0 + i * kRows + r;
+    if (j < used) {
+      const uint4* x = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(j) * 2 * D);
+      lo[i % kAhead] = x[0];
+      hi[i % kAhead] = x[D / E];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(i);
   double up[E], down[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) up[i] = down[i] = 0.0;
-  for (int g = 0; g < p.G; ++g) {
-    float x[E];
-    load16(static_cast<const T*>(p.q) + (row * p.G + g) * D + part * E, x);
+  const T* q = static_cast<const T*>(p.q) + row * p.G * D + part * E;
+  for (int g0 = 0; g0 < p.G; g0 += 4) {
+    float x[4][E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      // a NaN fails both comparisons and goes to both sums
-      up[i] += x[i] < 0.f ? 0.0 : static_cast<double>(x[i]);
-      down[i] += x[i] > 0.f ? 0.0 : static_cast<double>(x[i]);
-    }
+    for (int g = 0; g < 4; ++g) load16(q + min(g0 + g, p.G - 1) * D, x[g]);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (g0 + g < p.G)
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          // a NaN fails both comparisons and goes to both sums
+          up[i] += x[g][i] < 0.f ? 0.0 : static_cast<double>(x[g][i]);
+          down[i] += x[g][i] > 0.f ? 0.0 : static_cast<double>(x[g][i]);
+        }
   }
   // all threads take part in the sums over a row's lanes, with or without a block of their own
-#pragma unroll 2
-  for (int i0 = 0; i0 < kScoreBlocks; i0 += kRows) {
-    const int j = j0 + i0 + r;
-    if (j0 + i0 >= used) break;
-    double s = 0.0;
-    if (i0 + r < kScoreBlocks && j < used) {
-      float lo[E], hi[E];
-      load16(bounds + static_cast<int64_t>(j) * 2 * D, lo);
-      load16(bounds + static_cast<int64_t>(j) * 2 * D + D, hi);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        s += up[i] * static_cast<double>(hi[i]);
-        s += down[i] * static_cast<double>(lo[i]);
-      }
-    }
+  for (int i = 0; i < kIter; ++i) {
+    if (j0 + i * kRows >= used) break;
+    const int j = j0 + i * kRows + r;
+    double s = 0.0;
+    if (j < used) s = dot_piece<T>(lo[i % kAhead], down) + dot_piece<T>(hi[i % kAhead], up);
+    if (i + kAhead < kIter) load(i + kAhead);
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     const int back = newest >= j ? newest - j : newest - j + used;
-    if (part == 0 && i0 + r < kScoreBlocks && j < used)
+    if (part == 0 && j < used)
       p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last) ? ~0ull : sortable(s);
   }
 }
@@ -575,20 +658,21 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
   griddep_wait();
   SimtState<T, D> st;
   st.bind(smem);
+  __shared__ int flag[2];
   SeqWalk walk;
   walk.start(p, blockIdx.x);
   const int kvh = walk.item / p.groups, g0 = (walk.item - kvh * p.groups) * kSeqRows;
   const int rows = min(kSeqRows, p.G - g0);
+  int cut[2], n_cut = 0;  // sequences whose item this CTA holds a part of
   SeqRun run;
   while (walk.next(p, run)) {
     const int64_t qrow = static_cast<int64_t>(run.b) * p.Hq + kvh * p.G + g0;
-    const int n = seq_tokens(p, run.b);
     st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
     const int64_t row_elems = static_cast<int64_t>(p.Hkv) * D;
     const int64_t base = (static_cast<int64_t>(run.b) * p.W * p.Hkv + kvh) * D;
     const int64_t ebase = (static_cast<int64_t>(run.b) * p.Hkv + kvh) * p.W;
     for (int t = run.t0; t < run.t0 + run.tiles; ++t) {
-      auto slot = [&](int r) { return seq_slot(p, run.b, kvh, n, t, r); };
+      auto slot = [&](int r) { return seq_slot(p, run.b, kvh, run.tokens, t, r); };
       auto load = [&](const void* cache, const uint8_t* exps) {
         const uint8_t* rows8 = static_cast<const uint8_t*>(cache) + base * (KIND == SEQ_KV8 ? 1 : sizeof(T));
         simt_load<T, D, KIND>(st.tile, rows8, row_elems, KIND == SEQ_KV8 ? exps + ebase : nullptr, slot);
@@ -600,14 +684,37 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
       if (run.slot < 0) {
         put_f32(static_cast<T*>(p.out) + (qrow + h) * D + d, o / l);
       } else {
-        const int64_t at = static_cast<int64_t>(run.slot) * kSeqRows + h;
+        const int64_t at = static_cast<int64_t>(run.slot) * p.part_rows + h;
         p.part_o[at * D + d] = o;
-        if (d == 0) {
-          p.part_ml[at * 2] = m;
-          p.part_ml[at * 2 + 1] = l;
-        }
+        if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
       }
     });
+    if (run.slot >= 0 && p.N == 0) cut[n_cut++ & 1] = run.b;
+  }
+  if (n_cut == 0) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x < n_cut) {
+    const int b = threadIdx.x == 0 ? cut[0] : cut[1];
+    flag[threadIdx.x] = atomicAdd(p.count + b * p.items + walk.item, 1) == p.own[b].y - 1;
+  }
+  __syncthreads();
+  __threadfence();
+  const int lane = threadIdx.x & 31;
+  for (int i = 0; i < n_cut; ++i) {
+    if (!flag[i]) continue;
+    const int b = i == 0 ? cut[0] : cut[1];
+    const int2 own = p.own[b];
+    for (int h = threadIdx.x >> 5; h < rows; h += kSimtThreads / 32) {
+      const SeqPieces at{p, b, walk.item, h, own};
+      float acc[D / 32], M, L;
+      merge_pieces<D>(
+          own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },
+          [&](int k) { return p.part_ml + at.at(k) * 2; }, acc, M, L);
+      T* out = static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.Hq + kvh * p.G + g0 + h) * D + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) put_f32(out + e, acc[e] / L);
+    }
   }
 }
 
@@ -649,14 +756,11 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
   });
 }
 
-// ---------------------------------------------------------------- merge
-// sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the pieces of a (sequence, query
-// head): those of its item in the order of the tiles, then the prefix's.  One warp, or up
-// to 8 where there are many pieces; a lane holds one piece's weight, and the warp adds
-// the pieces' outputs with independent loads.  Items that one CTA held whole are written
-// already; an idle row's output is zero.
+// ---------------------------------------------------------------- merge with the prefix
+// The pieces of every (sequence, query head): those of its item in the order of the
+// tiles, then the prefix's; one warp, or up to 8 where there are many.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) seq_merge_kernel(const __grid_constant__ SeqParams p) {
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
   constexpr int E = D / 32;
   __shared__ float part[8][D + 2];
@@ -666,61 +770,16 @@ __global__ void __launch_bounds__(256) seq_merge_kernel(const __grid_constant__ 
   const bool mine = u < static_cast<int64_t>(p.B) * p.Hq;
   const int b = mine ? static_cast<int>(u / p.Hq) : 0, h = mine ? static_cast<int>(u - static_cast<int64_t>(b) * p.Hq) : 0;
   const int kvh = h / p.G, g = h - kvh * p.G;
-  const int item = kvh * p.groups + g / kSeqRows, row = g % kSeqRows;
   griddep_wait();
-  const int t = p.cum[b], tiles = p.cum[b + 1] - t, total = p.cum[p.B];
-  int pieces = 0, c0 = 0;
-  if (mine && tiles > 0) {
-    const int teams = seq_teams(p, total);
-    c0 = seq_owner(t, total, teams);
-    pieces = seq_owner(t + tiles - 1, total, teams) - c0 + 1;
-  }
-  const int all = pieces == 0 || (pieces == 1 && p.N == 0) ? 0 : pieces + p.splits;
-  float M = -INFINITY, L = 0.f, acc[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) acc[i] = 0.f;
-  for (int i0 = wi; i0 < all; i0 += 32 * p.merge_warps) {
-    const int i = i0 + lane * p.merge_warps;
-    const float *o = p.part_o, *ml = nullptr;
-    if (i < pieces) {
-      const int64_t slot = pieces == 1 ? 2 * p.ctas + static_cast<int64_t>(b) * p.items + item
-                                       : 2 * (static_cast<int64_t>(c0 + i) * p.items + item) + (i == 0 ? 1 : 0);
-      o = p.part_o + (slot * kSeqRows + row) * D;
-      ml = p.part_ml + (slot * kSeqRows + row) * 2;
-    } else if (i < all) {
-      const int64_t at = static_cast<int64_t>(i - pieces) * p.B * p.Hq + u;
-      o = p.pre_o + at * D;
-      ml = p.pre_ml + at * 2;
-    }
-    float m = -INFINITY, l = 0.f;
-    if (ml) {
-      const float2 v = *reinterpret_cast<const float2*>(ml);
-      m = v.x;
-      l = v.y;
-    }
-    float top = m;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    top = fmaxf(top, M);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float w = exp2f(m - ref), keep = exp2f(M - ref);
-    float sum = w * l;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    L = L * keep + sum;
-    M = top;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= keep;
-    const int n = min(32, (all - i0 + p.merge_warps - 1) / p.merge_warps);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float* ok =
-          reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k)) + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, ok[e], acc[e]);
-    }
-  }
+  const int2 own = p.own[b];
+  const int pieces = mine ? own.y : 0;  // none: an idle row, written already
+  const SeqPieces at{p, b, kvh * p.groups + g / kSeqRows, g % kSeqRows, own};
+  auto prefix = [&](int i) { return static_cast<int64_t>(i - pieces) * p.B * p.Hq + u; };
+  float acc[E], M, L;
+  merge_pieces<D>(
+      pieces ? pieces + p.splits : 0, p.merge_warps, wi, lane,
+      [&](int i) { return i < pieces ? p.part_o + at.at(i) * D : p.pre_o + prefix(i) * D; },
+      [&](int i) { return i < pieces ? p.part_ml + at.at(i) * 2 : p.pre_ml + prefix(i) * 2; }, acc, M, L);
   if (p.merge_warps > 1) {
 #pragma unroll
     for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
@@ -743,15 +802,10 @@ __global__ void __launch_bounds__(256) seq_merge_kernel(const __grid_constant__ 
       for (int e = 0; e < E; ++e) acc[e] += w * part[warp + k][lane * E + e];
     }
   }
-  if (!mine) return;
+  if (pieces == 0) return;
   T* out = static_cast<T*>(p.out) + u * D + lane * E;
-  if (pieces == 0) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) put_f32(out + e, 0.f);
-  } else if (all > 0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) put_f32(out + e, acc[e] / L);
-  }
+  for (int e = 0; e < E; ++e) put_f32(out + e, acc[e] / L);
 }
 
 // ---------------------------------------------------------------- host
@@ -760,7 +814,7 @@ size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // The device buffers of a step inside the caller's workspace, in this order.
 struct SeqLayout {
-  size_t cum, share, part_o, part_ml, pre_o, pre_ml, score, q8, q_scale, bytes;
+  size_t share, own, count, part_o, part_ml, pre_o, pre_ml, score, q8, q_scale, bytes;
 };
 
 // Pieces of the prefix.  CUDA cores: enough for three CTAs per SM.  Tensor cores: one
@@ -796,10 +850,11 @@ SeqLayout seq_layout(const SeqParams& p, int D, bool kv8) {
   };
   const size_t slots = 2 * static_cast<size_t>(std::max(kSeqMaxCtas, p.items)) + (p.N > 0 ? static_cast<size_t>(p.B) * p.items : 0);
   const size_t pre = static_cast<size_t>(p.splits) * p.B * p.Hq;
-  l.cum = take((static_cast<size_t>(p.B) + 1) * sizeof(int));
   l.share = take(kSeqMaxCtas * sizeof(int4));
-  l.part_o = take(slots * kSeqRows * D * sizeof(float));
-  l.part_ml = take(slots * kSeqRows * 2 * sizeof(float));
+  l.own = take(static_cast<size_t>(p.B) * sizeof(int2));
+  l.count = take(static_cast<size_t>(p.B) * p.items * sizeof(int));
+  l.part_o = take(slots * p.part_rows * D * sizeof(float));
+  l.part_ml = take(slots * p.part_rows * 2 * sizeof(float));
   l.pre_o = take(pre * D * sizeof(float));
   l.pre_ml = take(pre * 2 * sizeof(float));
   l.score = take(p.block ? static_cast<size_t>(p.B) * p.Hkv * p.n_blocks * sizeof(uint64_t) : 0);
@@ -819,8 +874,10 @@ swa_status seq_sizes(SeqParams& p, int D, int dtype) {
   if (dtype == SWA_F32 && D != 32 && D != 64 && D != 128) return SWA_ERR_UNSUPPORTED;
   p.groups = cdiv(p.G, kSeqRows);
   p.items = p.Hkv * p.groups;
-  if (p.Hq > 65535 || static_cast<int64_t>(p.B) * p.Hq > (1ll << 26) ||
-      static_cast<int64_t>(p.B) * (p.W / kSeqKeys + 2) > 0x7fffffffll ||
+  p.part_rows = std::min(p.G, kSeqRows);
+  if (p.Hq > 65535 ||
+      static_cast<int64_t>(p.B) * p.items > 0x3fffffffll || static_cast<int64_t>(p.B) * p.Hq > (1ll << 26) ||
+      static_cast<int64_t>(p.B) * (p.W / kSeqKeys + 2 + kSeqStart) > 0x7fffffffll ||
       static_cast<int64_t>(p.W) * p.Hkv * D > (1ll << 37))
     return SWA_ERR_SHAPE;
   p.splits = prefix_pieces(p, dtype == SWA_BF16);
@@ -843,9 +900,6 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
   const int ctas = kTc ? seq_tc_ctas(D, p.G, KIND == SEQ_KV8, device_sms()) : std::min(3 * device_sms(), kSeqMaxCtas);
   p.teams = std::max(1, ctas / p.items);
   p.ctas = p.teams * p.items;
-  // pieces of a row: the prefix's, and its share of the teams; a warp for every four
-  const int pieces = p.splits + p.teams / p.B + 1;
-  p.merge_warps = pieces <= 4 ? 1 : pieces <= 8 ? 2 : pieces <= 16 ? 4 : 8;
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv;
   int launches = 1;
   cudaError_t e;
@@ -886,11 +940,17 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
       e = launch_after(seq_simt_kernel<T, D, KIND>, dim3(p.ctas), dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
     ++launches;
   }
-  if (e == cudaSuccess) {
-    const int64_t heads = static_cast<int64_t>(p.B) * p.Hq;
-    const int per = 8 / p.merge_warps;
-    e = launch_after(seq_merge_kernel<T, D>, dim3(static_cast<unsigned>((heads + per - 1) / per)), dim3(256), 0, st, p);
-    ++launches;
+  if constexpr (KIND == SEQ_PLAIN) {
+    if (e == cudaSuccess && p.N > 0) {
+      // pieces of a row: the prefix's, and its share of the teams; a warp for every four
+      const int pieces = p.splits + p.teams / p.B + 1;
+      p.merge_warps = pieces <= 4 ? 1 : pieces <= 8 ? 2 : pieces <= 16 ? 4 : 8;
+      const int64_t heads = static_cast<int64_t>(p.B) * p.Hq;
+      const int per = 8 / p.merge_warps;
+      e = launch_after(prefix_merge_kernel<T, D>, dim3(static_cast<unsigned>((heads + per - 1) / per)), dim3(256), 0, st,
+                       p);
+      ++launches;
+    }
   }
   count_launches(launches);
   return e;
@@ -917,8 +977,9 @@ swa_status seq_step(SeqParams& p, int D, int dtype, void* workspace, size_t work
   if (!al16(workspace)) return SWA_ERR_ARG;
   if (const int ds = device_ready_status(&p.err)) return static_cast<swa_status>(ds);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.cum = reinterpret_cast<int*>(ws + l.cum);
   p.share = reinterpret_cast<int4*>(ws + l.share);
+  p.own = reinterpret_cast<int2*>(ws + l.own);
+  p.count = reinterpret_cast<int*>(ws + l.count);
   p.part_o = reinterpret_cast<float*>(ws + l.part_o);
   p.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
   p.pre_o = reinterpret_cast<float*>(ws + l.pre_o);

@@ -47,11 +47,9 @@ namespace swa {
 namespace {
 
 constexpr int kThreads = 192;
+constexpr int kBoxRows = 32;    // rows that one load brings
 constexpr int kN = kSeqCols;  // columns of S^T
 
-#ifndef SWA_SEQ_CTAS8
-#define SWA_SEQ_CTAS8 4
-#endif
 template <int D, int GP, bool KV8>
 struct SeqTcPlan {
   static constexpr int kElem = KV8 ? 1 : 2;
@@ -60,8 +58,12 @@ struct SeqTcPlan {
   static constexpr int kSubs = kRowBytes / kSubBytesRow;
   static constexpr int kSub = kSeqKeys * kSubBytesRow;
   static constexpr int kUnit = kSubs * kSub;                          // a K or a V tile
-  static constexpr int kPerSm = kUnit > 16 * 1024 ? 2 : (GP == 8 ? 3 : (KV8 ? SWA_SEQ_CTAS8 : 4));
-  static constexpr int kUnits = (kUnit > 16 * 1024 ? 96 : (kPerSm == 4 ? 48 : (KV8 ? 56 : 64))) * 1024 / kUnit;
+  // CTAs per SM, 48 KB of ring each, where a tile has up to 16 KB.  The softmax of a tile
+  // is a chain of latencies (0.45 us) that the CTAs overlap; of 2, 3 and 4 CTAs with 192,
+  // 144 and 192 KB of ring an SM, 3 read the 8-bit cache of 64 x 4096 x 8 x 128 fastest
+  // (100, 96 and 102 us: more streams only disturb one another in memory).
+  static constexpr int kPerSm = kUnit > 16 * 1024 ? 2 : 3;
+  static constexpr int kUnits = (kUnit > 16 * 1024 ? 96 : 48) * 1024 / kUnit;
   static constexpr int kOCols = (KV8 ? 3 : 1) * GP;                   // columns of O^T that count
   static constexpr int kON = kOCols > 16 ? 32 : 16;
   // The products take 16 (or 32) rows of Q and P^T; those behind the ones that count are
@@ -76,7 +78,8 @@ struct SeqTcPlan {
   static constexpr int kOffRed = kOffQ + 2 * kQ;  // [2][4][8] tile maxima, [4][8] row sums
   static constexpr int kOffBar = kOffRed + 3 * 4 * kSeqRows * 4;
   static constexpr int kNumBars = 2 + 2 + 2 * kUnits + 2 + 2 + 2 + 4;
-  static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+  static constexpr int kOffFlag = kOffBar + kNumBars * 8;  // which of the two cut items this CTA merges
+  static constexpr int kOffTmem = kOffFlag + 16;
   static constexpr int kReadEnd = kOffQ + kQ + (kSubs - 1) * kQSub + kN * kSubBytesRow;
   static constexpr int kBytes = kOffTmem + 16 > kReadEnd ? kOffTmem + 16 : kReadEnd;
   static constexpr int kSmem = kBytes + 1024;  // + alignment slack
@@ -217,21 +220,22 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
   SeqWalk walk;
   walk.start(p, blockIdx.x);
   SeqRun run;
-  // The ring's units are K and V tiles in the order the products take them:
+  // The ring holds K and V tiles in the order the products take them:
   // K_0, K_1 V_0, K_2 V_1, ..., V_last (tile j of the CTA's share).
   const int last = walk.left - 1;
   auto k_unit = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
   auto v_unit = [&](int j) { return j == last ? 2 * j + 1 : 2 * j + 2; };
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    // the lanes issue the boxes of a tile side by side: one box of 128 rows per sub-tile,
-    // or one per selected block (8 of them at most, 16 pieces)
+    // the lanes issue the boxes of a tile side by side: of 32 rows, so that an item's
+    // last tile brings few rows behind the keys, or of a selected block (8 of them at
+    // most, 16 pieces)
     if (lane == 0) {
       tma_prefetch_desc(&tp.tm_k);
       tma_prefetch_desc(&tp.tm_v);
       tma_prefetch_desc(&tp.tm_q);
     }
-    const int rows = p.block ? p.block : kSeqKeys;  // of a box
+    const int rows = p.block ? p.block : kBoxRows;
     const int per_tile = kSeqKeys / rows;
     const int box = lane / PL::kSubs, sub = lane % PL::kSubs;
     const uint32_t dst = base + sub * PL::kSub + box * rows * PL::kSubBytesRow;
@@ -266,11 +270,13 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       }
       ++lu;
       const int* sel = p.block ? p.selected + (static_cast<int64_t>(run.b) * p.Hkv + kvh) * p.n_select : nullptr;
-      const int n_blocks = p.block ? min((seq_tokens(p, run.b) + p.block - 1) / p.block, p.n_select) : 0;
+      // boxes of the whole item
+      const int n_boxes = p.block ? min((run.tokens + p.block - 1) / p.block, p.n_select)
+                                  : (run.tokens + kBoxRows - 1) / kBoxRows;
       for (int j = 0; j < run.tiles && ok; ++j, ++jj) {
         const int first = (run.t0 + j) * per_tile;  // box of the item
-        const int boxes = p.block ? min(per_tile, n_blocks - first) : 1;
-        const int row = box >= boxes ? -1 : (p.block ? sel[first + box] * p.block : first * kSeqKeys);
+        const int boxes = min(per_tile, n_boxes - first);
+        const int row = box >= boxes ? -1 : (p.block ? sel[first + box] * p.block : (first + box) * kBoxRows);
         ok = load(&tp.tm_k, run.b, kvh, boxes, row);
         if (ok && jj > 0) ok = load(&tp.tm_v, b1, h1, boxes1, row1);
         b1 = run.b;
@@ -380,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tO = tmem + lane_off + 2 * kN;
     float* red = reinterpret_cast<float*>(gbase + PL::kOffRed);  // [2][4][8] maxima, then [4][8] sums
+    const int kvh = walk.item;
     int jj = 0, nu = 0, nx = 0;  // tiles, finished items, exchanges so far
     bool ok = true;
     auto exchange = [&]() -> bool {
@@ -389,39 +396,49 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, ERR_WAIT_SOFTMAX));
     };
-    while (ok && walk.next(p, run)) {
-      const int kvh = walk.item, b = run.b;
+    int cut[2], n_cut = 0;  // sequences whose item this CTA holds a part of
+    // This key's place and exponents, and the queries' scales, are loaded a tile (a
+    // sequence) ahead of their use.
+    SeqRun ahead;
+    bool more = walk.next(p, ahead);
+    int slot = -1, ke = 127, ve = 127;
+    float scale[GP];
+    auto fetch = [&](const SeqRun& x, int t) {
+      slot = seq_slot(p, x.b, kvh, x.tokens, t, r);
+      if constexpr (KV8) {
+        ke = ve = 127;
+        if (slot >= 0) {
+          const int64_t at = (static_cast<int64_t>(x.b) * p.Hkv + kvh) * p.W + slot;
+          ke = p.k_exp[at];
+          ve = p.v_exp[at];
+        }
+      }
+    };
+    auto fetch_run = [&](const SeqRun& x) {
+      fetch(x, x.t0);
+#pragma unroll
+      for (int h = 0; h < GP; ++h)
+        scale[h] = KV8 ? (h < p.G ? p.q_scale[static_cast<int64_t>(x.b) * p.Hq + kvh * p.G + h] : 0.f) : 1.f;
+    };
+    if (more) fetch_run(ahead);
+    while (ok && more) {
+      run = ahead;
+      more = walk.next(p, ahead);
+      const int b = run.b;
       const int64_t qrow = static_cast<int64_t>(b) * p.Hq + kvh * p.G;
-      const int n_tokens = seq_tokens(p, b);
-      const int64_t ebase = (static_cast<int64_t>(b) * p.Hkv + kvh) * p.W;
       float m[GP], l[GP], c[GP];
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
         m[h] = -INFINITY;
         l[h] = 0.f;
-        c[h] = p.scale_log2;
-        if constexpr (KV8) c[h] *= h < p.G ? p.q_scale[qrow + h] : 0.f;
-      }
-      // this key's place and exponents, a tile ahead of their use
-      int slot = seq_slot(p, b, kvh, n_tokens, run.t0, r), ke = 127, ve = 127;
-      if (KV8 && slot >= 0) {
-        ke = p.k_exp[ebase + slot];
-        ve = p.v_exp[ebase + slot];
+        c[h] = p.scale_log2 * scale[h];
       }
       for (int j = 0; j < run.tiles; ++j, ++jj) {
         const int sb = jj & 1;
         const bool valid = slot >= 0;
         const int ke0 = ke, ve0 = ve;
-        if (j + 1 < run.tiles) {
-          slot = seq_slot(p, b, kvh, n_tokens, run.t0 + j + 1, r);
-          if (KV8) {
-            ke = ve = 127;
-            if (slot >= 0) {
-              ke = p.k_exp[ebase + slot];
-              ve = p.v_exp[ebase + slot];
-            }
-          }
-        }
+        if (j + 1 < run.tiles) fetch(run, run.t0 + j + 1);
+        else if (more) fetch_run(ahead);
         if (!wait(s_full(sb), (jj >> 1) & 1)) {
           ok = false;
           break;
@@ -591,18 +608,48 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
           if (run.slot < 0) {
             static_cast<__nv_bfloat16*>(p.out)[(qrow + h) * D + r] = __float2bfloat16_rn(o / l[h]);
           } else {
-            const int64_t at = static_cast<int64_t>(run.slot) * kSeqRows + h;
+            const int64_t at = static_cast<int64_t>(run.slot) * p.part_rows + h;
             p.part_o[at * D + r] = o;
-            if (r == 0) {
-              p.part_ml[at * 2] = m[h];
-              p.part_ml[at * 2 + 1] = l[h];
+            if (r == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m[h], l[h]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (run.slot >= 0 && p.N == 0) cut[n_cut++ & 1] = b;
+      // the sums are rewritten only after the next item's first exchange, which every
+      // thread reaches after reading them here
+    }
+    if (ok && n_cut > 0) {
+      // count the pieces once all threads' results are visible; who counts an item's last
+      // merges it, two heads a warp at most
+      int* flag = reinterpret_cast<int*>(gbase + PL::kOffFlag);
+      __threadfence();
+      if (exchange()) {
+        if (r < n_cut) {
+          const int b = r == 0 ? cut[0] : cut[1];
+          flag[r] = atomicAdd(p.count + b * p.items + kvh, 1) == p.own[b].y - 1;
+        }
+        if (exchange()) {
+          __threadfence();
+          for (int i = 0; i < n_cut; ++i) {
+            if (!flag[i]) continue;
+            const int b = i == 0 ? cut[0] : cut[1];
+            const int2 own = p.own[b];
+            for (int h = quarter; h < p.G; h += 4) {
+              const SeqPieces at{p, b, kvh, h, own};
+              float acc[D / 32], M, L;
+              merge_pieces<D>(
+                  own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },
+                  [&](int k) { return p.part_ml + at.at(k) * 2; }, acc, M, L);
+              uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) +
+                                                          (static_cast<int64_t>(b) * p.Hq + kvh * p.G + h) * D) +
+                              lane * (D / 64);
+#pragma unroll
+              for (int e = 0; e < D / 32; e += 2) dst[e / 2] = pack_bf16x2(acc[e] / L, acc[e + 1] / L);
             }
           }
         }
       }
-      // the sums are rewritten only after the next item's first exchange, which every
-      // thread reaches after reading them here
-      tc_fence_before();
     }
   }
 
@@ -668,7 +715,7 @@ cudaError_t launch_seq_tc(const SeqParams& s, int D, bool kv8, cudaStream_t st) 
                             static_cast<uint64_t>(s.B)};
   const uint64_t row = s.Hkv * D * e;
   const uint64_t strides[3] = {D * e, row, row * s.W};
-  const uint32_t box[4] = {cols, 1, static_cast<uint32_t>(s.block ? s.block : kSeqKeys), 1};
+  const uint32_t box[4] = {cols, 1, static_cast<uint32_t>(s.block ? s.block : kBoxRows), 1};
   const uint64_t qdims[2] = {static_cast<uint64_t>(D),
                              kv8 ? static_cast<uint64_t>(s.B) * s.Hkv * kN : static_cast<uint64_t>(s.B) * s.Hq};
   const uint64_t qstride[1] = {D * e};

@@ -276,3 +276,51 @@ def test_decode_sparse_matches_float64(swa, B, W, Hq, Hkv, D, dtype, block, n_se
     check_decode(out, ref, scale, dtype, what="sparse")
     np.testing.assert_array_equal(np64(k), kc)
     np.testing.assert_array_equal(np64(v), vc)
+
+
+@pytest.mark.parametrize("op", ["kv8", "prefix", "sparse"])
+@pytest.mark.parametrize("G,D,dtype", [(4, 128, BF16), (8, 64, BF16), (1, 64, BF16), (2, 128, F32)])
+def test_many_units_for_a_cta(swa, op, G, D, dtype):
+    """More work than CTAs: every CTA takes several chunks, of items that are cut and of whole ones.
+    Checked on the GPU in 64 bits."""
+    B, W, Hkv, N, block, n_select = 150, 2100, 4, 300, 32, 40
+    Hq = Hkv * G
+    g = torch.Generator(device="cuda").manual_seed(G * D)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    pos = torch.randint(0, W, (B,), generator=g, device="cuda")
+    pos[3], pos[4] = 10 * W, -1
+    q, kn, vn, out = rand(B, Hq, D), rand(B, Hkv, D), rand(B, Hkv, D), rand(B, Hq, D)
+    k, v = rand(B, W, Hkv, D), rand(B, W, Hkv, D)
+    kp, vp = rand(N, Hkv, D), rand(N, Hkv, D)
+    live, slot = torch.where(pos >= 0)[0], (pos % W)[pos >= 0]
+    n = torch.clamp(pos + 1, 0, W)
+    seen = (torch.arange(W, device="cuda") < n[:, None])[:, None, None]
+    if op == "kv8":
+        cache = new_cache8(B, W, Hkv, D)
+        swa.swa_kv8_write(k, v, *cache, torch.zeros_like(pos))
+        swa.swa_decode_kv8(q, kn, vn, *cache, pos, out)
+        k, v = (c.double() * torch.exp2(e.double().transpose(1, 2) - 127)[..., None] for c, e in (cache[:2], cache[2:]))
+    elif op == "prefix":
+        swa.swa_decode_prefix(q, kn, vn, kp, vp, k, v, pos, out)
+    else:
+        bounds = rand(B, Hkv, -(-W // block), 2, D)
+        swa.swa_block_bounds(k, torch.where(pos > 0, pos - 1, pos), bounds, block)
+        sel = torch.empty(B, Hkv, n_select, dtype=torch.int32, device="cuda")
+        swa.swa_decode_sparse(q, kn, vn, k, v, bounds, pos, out, sel, block)
+        picked = (sel[..., None] == torch.arange(bounds.shape[2], device="cuda")).any(2).repeat_interleave(block, 2)
+        seen = seen & picked[:, :, None, :W]
+        assert ((sel >= 0).sum(2) == torch.clamp((n + block - 1) // block, max=n_select)[:, None]).all()
+    torch.cuda.synchronize()
+    assert swa.swa_device_error_check() == 0
+    if op != "kv8":
+        assert torch.equal(k[live, slot], kn[live]) and torch.equal(v[live, slot], vn[live])
+    q64, k64, v64 = q.double().view(B, Hkv, G, D), k.double().transpose(1, 2), v.double().transpose(1, 2)
+    s = torch.where(seen, q64 @ k64.transpose(2, 3) / D ** 0.5, -float("inf"))
+    if op == "prefix":
+        s = torch.cat([s, torch.einsum("bhgd,nhd->bhgn", q64, kp.double()) / D ** 0.5], -1)
+        k64, v64 = (torch.cat([x, y.double().transpose(0, 1).expand(B, -1, -1, -1)], 2) for x, y in ((k64, kp), (v64, vp)))
+    p = torch.softmax(s, -1).nan_to_num() * (pos >= 0)[:, None, None, None]
+    ref, scale = p @ v64, p @ v64.abs()
+    check_decode(out, np64(ref).reshape(B, Hq, D), np64(scale).reshape(B, Hq, D), dtype,
+                 np64(q) if op == "kv8" else None, np64(k) if op == "kv8" else None, op)
+    assert (out[4] == 0).all()
