@@ -457,7 +457,7 @@ swa_status swa_rope_nd(const void* x, void* y, const int32_t* pos, long long tok
  * T tokens sequence b has (taken as 0 below 0 and as T above T); slots and rows
  * behind them, and all of an idle row, are left as they were.  Of a run longer than W
  * the last W tokens are kept.  dtype is that of k and v; head_dim 32, 64 or 128.
- * Errors: SWA_ERR_ARG, SWA_ERR_SHAPE (B over 65535), SWA_ERR_UNSUPPORTED. */
+ * Errors: SWA_ERR_ARG, SWA_ERR_SHAPE (B over 65535, T * Hkv 2^30 or more), SWA_ERR_UNSUPPORTED. */
 swa_status swa_kv8_write(const void* k, const void* v, void* k8, uint8_t* k_exp, void* v8, uint8_t* v_exp,
                          const long long* pos, const int32_t* count, int B, int T, int W, int Hkv, int head_dim,
                          int dtype, void* stream);

@@ -15,6 +15,7 @@ Tensor layouts follow the pages' contracts: tokens [B, S*P, heads, head_dim]
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import re
 
@@ -314,33 +315,49 @@ def swa_decode_noalloc(q, k_new, v_new, k_cache, v_cache, pos: int, out, stream=
 
 
 # ------------------------------------ rotary positions with several axes
-def _cuda(*tensors) -> torch.device:
-    """The CUDA device that all the tensors are on."""
-    dev = tensors[0].device
-    for t in tensors:
-        if not t.is_cuda or t.device != dev:
-            raise ValueError(f"tensors must be on one CUDA device, got {[str(t.device) for t in tensors]}")
-    return dev
+# The checks below are on the path of every decode step, where a call's launches take
+# a few microseconds: one loop over a call's tensors, sizes looked up once.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _like(what: str, t, shape, dtype) -> None:
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{what}: want {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+def _fit(*specs) -> tuple[int, list[int]]:
+    """(device index, addresses) of the tensors of ``specs``, (name, tensor, shape, dtype)
+    each: contiguous, and all on one CUDA device."""
+    dev, ptrs = specs[0][1].get_device(), []
+    for what, t, shape, dtype in specs:
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{what}: want {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{what} is on {t.device}: tensors must be on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: tensors must be contiguous")
+        ptrs.append(t.data_ptr())
+    return dev, ptrs
 
 
-def _on(dev: torch.device, stream, call):
-    """call(stream handle) with ``dev`` current; the handle is the device's current
-    stream where ``stream`` is None."""
-    if dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(dev):
-        return call(_stream(stream))
+def _run(name: str, dev: int, stream, *args) -> None:
+    """Call ``name`` with ``dev`` current, on ``stream`` or the device's current stream."""
+    if stream is not None:
+        handle = _stream(stream)
+    elif _raw_stream is not None:
+        handle = _raw_stream(dev)
+    else:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        status = getattr(_lib, name)(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib, name)(*args, handle)
+    if status != 0:
+        raise SwaError(status, name)
 
 
 def _token_rows(what: str, t) -> tuple[int, int]:
     """(tokens, elements between them) of t [..., heads, head_dim] whose rows are
     contiguous and whose leading axes step evenly from token to token."""
     H, D = t.shape[-2:]
+    if t.is_contiguous():
+        return (t.numel() // (H * D) if H * D else 0), H * D
     if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
     n, step = 1, H * D
@@ -355,124 +372,119 @@ def _token_rows(what: str, t) -> tuple[int, int]:
     return (0 if 0 in t.shape[:-2] else n), step
 
 
+@functools.lru_cache(maxsize=64)
+def _int32s(values: tuple):
+    return (C.c_int32 * max(1, len(values)))(*values)
+
+
 def swa_rope_nd(x, pos, pairs, theta: float = 10000.0, inverse: bool = False, out=None, stream=None) -> torch.Tensor:
     """Rotary positions with several axes: x [..., heads, head_dim] (token rows may be
     a slice of wider ones) turned by int32 positions pos [..., axes], ``pairs[a]``
     element pairs for axis a.  ``out`` may be x itself.  The gradient of the rotation
     is the call with ``inverse=True`` on the output's gradient (see include/swa.h)."""
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    dev = _cuda(x, pos, out)
-    _like("pos", pos, x.shape[:-2] + (len(pairs),), torch.int32)
-    _like("out", out, x.shape, x.dtype)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    axes = len(pairs)
+    dev, (at,) = _fit(("pos", pos, x.shape[:-2] + (axes,), torch.int32))
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"out: want {tuple(x.shape)} {x.dtype}, got {tuple(out.shape)} {out.dtype}")
+    if x.get_device() != dev or out.get_device() != dev:
+        raise ValueError(f"x is on {x.device}, out on {out.device}: tensors must be on one CUDA device")
     H, D = x.shape[-2:]
     (n, xs), (_, ys) = _token_rows("x", x), _token_rows("out", out)
-    _check(_on(dev, stream, lambda st: _lib.swa_rope_nd(
-        x.data_ptr(), out.data_ptr(), _ptr(pos), n, H, D, xs, ys, len(pairs),
-        (C.c_int32 * max(1, len(pairs)))(*pairs), float(theta), int(bool(inverse)), _dtype_code(x), st)), "swa_rope_nd")
+    _run("swa_rope_nd", dev, stream, x.data_ptr(), out.data_ptr(), at, n, H, D, xs, ys, axes, _int32s(tuple(pairs)),
+         theta, 1 if inverse else 0, _dtype_code(x))
     return out
 
 
 # ------------------------------------------------- rolling cache in 8 bits
-def _cache8(k8, k_exp, v8, v_exp) -> tuple[int, int, int, int]:
-    B, W, Hkv, D = k8.shape
-    _like("k8", k8, (B, W, Hkv, D), torch.float8_e4m3fn)
-    _like("v8", v8, (B, W, Hkv, D), torch.float8_e4m3fn)
-    _like("k_exp", k_exp, (B, Hkv, W), torch.uint8)
-    _like("v_exp", v_exp, (B, Hkv, W), torch.uint8)
-    return B, W, Hkv, D
+_E4M3, _U8, _I64, _I32 = torch.float8_e4m3fn, torch.uint8, torch.int64, torch.int32
 
 
-def _run8(fn, name, k, v, k8, k_exp, v8, v_exp, pos, count, stream, write):
-    B, W, Hkv, D = _cache8(k8, k_exp, v8, v_exp)
+def _cache8(k8, k_exp, v8, v_exp):
+    """Sizes of an 8-bit cache, and what _fit checks of it."""
+    B, W, Hkv, D = shape = k8.shape
+    return B, W, Hkv, D, (("k8", k8, shape, _E4M3), ("k_exp", k_exp, (B, Hkv, W), _U8), ("v8", v8, shape, _E4M3),
+                          ("v_exp", v_exp, (B, Hkv, W), _U8))
+
+
+def _run8(name, k, v, k8, k_exp, v8, v_exp, pos, count, stream, write):
+    B, W, Hkv, D, cache = _cache8(k8, k_exp, v8, v_exp)
     T = k.shape[1] if k.dim() == 4 else -1
-    _like("k", k, (B, T, Hkv, D), k.dtype)
-    _like("v", v, (B, T, Hkv, D), k.dtype)
-    _like("pos", pos, (B,), torch.int64)
-    if count is not None:
-        _like("count", count, (B,), torch.int32)
-    dev = _cuda(k, v, k8, k_exp, v8, v_exp, pos, *([] if count is None else [count]))
-    cache = [_ptr(k8), _ptr(k_exp), _ptr(v8), _ptr(v_exp)]
-    run = [_ptr(k), _ptr(v)]
-    at = [_ptr(pos), _ptr(count)]
-    args = run + cache + at if write else cache + at + run
-    _check(_on(dev, stream, lambda st: fn(*args, B, T, W, Hkv, D, _dtype_code(k), st)), name)
+    run = (("k", k, (B, T, Hkv, D), k.dtype), ("v", v, (B, T, Hkv, D), k.dtype))
+    at = (("pos", pos, (B,), _I64),) + (() if count is None else (("count", count, (B,), _I32),))
+    dev, ptrs = _fit(*(run + cache + at if write else cache + at + run))
+    if count is None:
+        ptrs.insert(7 if write else 5, None)
+    _run(name, dev, stream, *ptrs, B, T, W, Hkv, D, _dtype_code(k))
 
 
 def swa_kv8_write(k, v, k8, k_exp, v8, v_exp, pos, count=None, stream=None) -> None:
     """Quantise tokens k, v [B, T, Hkv, D] into the 8-bit rolling cache at positions
     pos[b] + t (k8, v8 [B, W, Hkv, D] float8_e4m3fn, k_exp, v_exp [B, Hkv, W] uint8;
     pos [B] int64, count [B] int32 or None; see include/swa.h)."""
-    _run8(_lib.swa_kv8_write, "swa_kv8_write", k, v, k8, k_exp, v8, v_exp, pos, count, stream, True)
+    _run8("swa_kv8_write", k, v, k8, k_exp, v8, v_exp, pos, count, stream, True)
 
 
 def swa_kv8_read(k8, k_exp, v8, v_exp, pos, k, v, count=None, stream=None):
     """Read the tokens at positions pos[b] + t back from the 8-bit cache into k, v
     [B, T, Hkv, D]; rows behind count[b] are left as they were."""
-    _run8(_lib.swa_kv8_read, "swa_kv8_read", k, v, k8, k_exp, v8, v_exp, pos, count, stream, False)
+    _run8("swa_kv8_read", k, v, k8, k_exp, v8, v_exp, pos, count, stream, False)
     return k, v
 
 
 # ---------------------------------- decode steps with a position per sequence
+@functools.lru_cache(maxsize=256)
 def swa_decode_kv8_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, W: int) -> int:
     return int(_lib.swa_decode_kv8_workspace_bytes(B, Hq, Hkv, head_dim, W))
 
 
+@functools.lru_cache(maxsize=256)
 def swa_decode_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, W: int, N: int) -> int:
     return int(_lib.swa_decode_prefix_workspace_bytes(B, Hq, Hkv, head_dim, W, N))
 
 
+@functools.lru_cache(maxsize=256)
 def swa_decode_sparse_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, W: int, block: int) -> int:
     return int(_lib.swa_decode_sparse_workspace_bytes(B, Hq, Hkv, head_dim, W, block))
 
 
-def _step_args(q, k_new, v_new, pos, out, Hkv: int, *caches):
-    """Checks what the decode steps have in common; (device, B, Hq, D)."""
-    B, Hq, D = q.shape
-    _like("k_new", k_new, (B, Hkv, D), q.dtype)
-    _like("v_new", v_new, (B, Hkv, D), q.dtype)
-    _like("pos", pos, (B,), torch.int64)
-    _like("out", out, (B, Hq, D), q.dtype)
-    return _cuda(q, k_new, v_new, pos, out, *caches), B, Hq, D
-
-
-def _scratch(workspace, nbytes: int, dev, stream):
+def _scratch(workspace, nbytes: int, like, dev: int, stream):
+    """The address and size of the step's workspace, allocated beside ``like`` if there is none."""
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=like.device)
         if stream is not None:  # the memory may not be handed on before that stream is through with it
             workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream), device=dev))
-        return workspace
-    if workspace.device != dev:
-        raise ValueError("workspace is on another device")
-    return workspace
+                                    else torch.cuda.ExternalStream(int(stream), device=like.device))
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: want a contiguous tensor on the device of the others")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def swa_decode_kv8(q, k_new, v_new, k8, k_exp, v8, v_exp, pos, out, workspace=None, stream=None):
     """One token per sequence at pos[b] on the 8-bit rolling cache (layouts as
     swa_kv8_write), which is updated in place; q, out [B, Hq, D] (see include/swa.h)."""
-    Bc, W, Hkv, Dc = _cache8(k8, k_exp, v8, v_exp)
-    dev, B, Hq, D = _step_args(q, k_new, v_new, pos, out, Hkv, k8, k_exp, v8, v_exp)
-    _like("k8", k8, (B, W, Hkv, D), torch.float8_e4m3fn)
-    ws = _scratch(workspace, _lib.swa_decode_kv8_workspace_bytes(B, Hq, Hkv, D, W), dev, stream)
-    _check(_on(dev, stream, lambda st: _lib.swa_decode_kv8(
-        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k8), _ptr(k_exp), _ptr(v8), _ptr(v_exp), _ptr(pos), W, B, Hq, Hkv, D,
-        _ptr(out), _ptr(ws), ws.nbytes, _dtype_code(q), st)), "swa_decode_kv8")
+    B, W, Hkv, D, cache = _cache8(k8, k_exp, v8, v_exp)
+    Hq, dt = q.shape[1], q.dtype
+    dev, ptrs = _fit(("q", q, (B, Hq, D), dt), ("k_new", k_new, (B, Hkv, D), dt), ("v_new", v_new, (B, Hkv, D), dt),
+                     *cache, ("pos", pos, (B,), _I64), ("out", out, (B, Hq, D), dt))
+    ws, at, nbytes = _scratch(workspace, swa_decode_kv8_workspace_bytes(B, Hq, Hkv, D, W), q, dev, stream)
+    _run("swa_decode_kv8", dev, stream, *ptrs[:8], W, B, Hq, Hkv, D, ptrs[8], at, nbytes, _dtype_code(q))
     return out
 
 
 def swa_decode_prefix(q, k_new, v_new, k_prefix, v_prefix, k_cache, v_cache, pos, out, workspace=None, stream=None):
     """One token per sequence at pos[b] of its own rolling cache [B, W, Hkv, D], all of
     them behind the shared prefix [N, Hkv, D] (see include/swa.h)."""
-    W, Hkv = k_cache.shape[1:3]
-    dev, B, Hq, D = _step_args(q, k_new, v_new, pos, out, Hkv, k_cache, v_cache, k_prefix, v_prefix)
-    N = k_prefix.shape[0]
-    for what, t, shape in (("k_cache", k_cache, (B, W, Hkv, D)), ("v_cache", v_cache, (B, W, Hkv, D)),
-                           ("k_prefix", k_prefix, (N, Hkv, D)), ("v_prefix", v_prefix, (N, Hkv, D))):
-        _like(what, t, shape, q.dtype)
-    ws = _scratch(workspace, _lib.swa_decode_prefix_workspace_bytes(B, Hq, Hkv, D, W, N), dev, stream)
-    _check(_on(dev, stream, lambda st: _lib.swa_decode_prefix(
-        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_prefix), _ptr(v_prefix), N, _ptr(k_cache), _ptr(v_cache), _ptr(pos),
-        W, B, Hq, Hkv, D, _ptr(out), _ptr(ws), ws.nbytes, _dtype_code(q), st)), "swa_decode_prefix")
+    B, W, Hkv, D = cache = k_cache.shape
+    Hq, dt, N = q.shape[1], q.dtype, k_prefix.shape[0]
+    dev, ptrs = _fit(("q", q, (B, Hq, D), dt), ("k_new", k_new, (B, Hkv, D), dt), ("v_new", v_new, (B, Hkv, D), dt),
+                     ("k_prefix", k_prefix, (N, Hkv, D), dt), ("v_prefix", v_prefix, (N, Hkv, D), dt),
+                     ("k_cache", k_cache, cache, dt), ("v_cache", v_cache, cache, dt), ("pos", pos, (B,), _I64),
+                     ("out", out, (B, Hq, D), dt))
+    ws, at, nbytes = _scratch(workspace, swa_decode_prefix_workspace_bytes(B, Hq, Hkv, D, W, N), q, dev, stream)
+    _run("swa_decode_prefix", dev, stream, *ptrs[:5], N, *ptrs[5:8], W, B, Hq, Hkv, D, ptrs[8], at, nbytes,
+         _dtype_code(q))
     return out
 
 
@@ -482,17 +494,15 @@ def swa_decode_sparse(q, k_new, v_new, k_cache, v_cache, bounds, pos, out, selec
     score chooses per (sequence, KV head); ``selected`` [B, Hkv, n_select] int32
     receives them, ``bounds`` [B, Hkv, ceil(W / block), 2, D] is kept up (see
     include/swa.h and swa_block_bounds)."""
-    W, Hkv = k_cache.shape[1:3]
-    dev, B, Hq, D = _step_args(q, k_new, v_new, pos, out, Hkv, k_cache, v_cache, bounds, selected)
-    for what, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _like(what, t, (B, W, Hkv, D), q.dtype)
-    _like("bounds", bounds, (B, Hkv, -(-W // max(1, block)), 2, D), q.dtype)
-    _like("selected", selected, (B, Hkv, selected.shape[-1]), torch.int32)
-    ws = _scratch(workspace, _lib.swa_decode_sparse_workspace_bytes(B, Hq, Hkv, D, W, block), dev, stream)
-    _check(_on(dev, stream, lambda st: _lib.swa_decode_sparse(
-        _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(bounds), _ptr(pos), W, block,
-        selected.shape[-1], n_first, n_last, B, Hq, Hkv, D, _ptr(out), _ptr(selected), _ptr(ws), ws.nbytes,
-        _dtype_code(q), st)), "swa_decode_sparse")
+    B, W, Hkv, D = cache = k_cache.shape
+    Hq, dt, n_select = q.shape[1], q.dtype, selected.shape[-1]
+    dev, ptrs = _fit(("q", q, (B, Hq, D), dt), ("k_new", k_new, (B, Hkv, D), dt), ("v_new", v_new, (B, Hkv, D), dt),
+                     ("k_cache", k_cache, cache, dt), ("v_cache", v_cache, cache, dt),
+                     ("bounds", bounds, (B, Hkv, -(-W // max(1, block)), 2, D), dt), ("pos", pos, (B,), _I64),
+                     ("out", out, (B, Hq, D), dt), ("selected", selected, (B, Hkv, n_select), _I32))
+    ws, at, nbytes = _scratch(workspace, swa_decode_sparse_workspace_bytes(B, Hq, Hkv, D, W, block), q, dev, stream)
+    _run("swa_decode_sparse", dev, stream, *ptrs[:7], W, block, n_select, n_first, n_last, B, Hq, Hkv, D, *ptrs[7:], at,
+         nbytes, _dtype_code(q))
     return out
 
 
@@ -500,10 +510,9 @@ def swa_block_bounds(k_cache, pos, bounds, block: int, stream=None) -> torch.Ten
     """Elementwise lowest and highest key of every block of a cache [B, W, Hkv, D] whose
     newest positions are pos, for swa_decode_sparse."""
     B, W, Hkv, D = k_cache.shape
-    _like("pos", pos, (B,), torch.int64)
-    _like("bounds", bounds, (B, Hkv, -(-W // max(1, block)), 2, D), k_cache.dtype)
-    _check(_on(_cuda(k_cache, pos, bounds), stream, lambda st: _lib.swa_block_bounds(
-        _ptr(k_cache), _ptr(pos), _ptr(bounds), W, block, B, Hkv, D, _dtype_code(k_cache), st)), "swa_block_bounds")
+    dev, ptrs = _fit(("k_cache", k_cache, k_cache.shape, k_cache.dtype), ("pos", pos, (B,), _I64),
+                     ("bounds", bounds, (B, Hkv, -(-W // max(1, block)), 2, D), k_cache.dtype))
+    _run("swa_block_bounds", dev, stream, *ptrs, W, block, B, Hkv, D, _dtype_code(k_cache))
     return bounds
 
 

@@ -13,6 +13,7 @@
 #include <cstdint>
 
 #include "../../include/swa.h"
+#include "fastdiv.cuh"
 #include "internal.h"
 #include "kv8.cuh"
 
@@ -28,6 +29,7 @@ struct RunParams {
   const long long* pos;   // [B]
   const int* count;       // [B] or null
   int B, T, W, Hkv;
+  FastDiv heads;          // Hkv
 };
 
 SWA_DEV int run_length(const RunParams& p, int b) {
@@ -61,10 +63,9 @@ template <int D>
 struct RunRows {
   static constexpr int kLanes = D / 16;
   static constexpr int kStep = kRunThreads / kLanes;
-  int64_t r0;
-  int part;
+  int r0, part;
   SWA_DEV RunRows()
-      : r0(static_cast<int64_t>(blockIdx.x) * (kStep * kRunRows) + threadIdx.x / kLanes), part(threadIdx.x % kLanes) {}
+      : r0(static_cast<int>(blockIdx.x) * (kStep * kRunRows) + threadIdx.x / kLanes), part(threadIdx.x % kLanes) {}
 };
 
 // grid: x over the rows of one sequence, y the sequence, z K or V
@@ -75,22 +76,22 @@ __global__ void __launch_bounds__(kRunThreads) kv8_write_kernel(const __grid_con
   const int b = blockIdx.y;
   const bool is_v = blockIdx.z;
   const long long pos = p.pos[b];
-  const int n = run_length(p, b);
-  if (pos < 0 || (at.r0 - threadIdx.x / R::kLanes) >= static_cast<int64_t>(n) * p.Hkv) return;
+  // of a run longer than the window only the last W tokens stay
+  const int end = run_length(p, b) * p.Hkv, skip = max(0, run_length(p, b) - p.W);
+  if (pos < 0 || at.r0 - static_cast<int>(threadIdx.x) / R::kLanes >= end) return;
   const T* x = static_cast<const T*>(is_v ? p.x[1] : p.x[0]) + static_cast<int64_t>(b) * p.T * p.Hkv * D + at.part * 16;
   Raw16<T> raw[kRunRows];
   bool live[kRunRows];
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
-    const int64_t r = at.r0 + i * R::kStep;
-    // of a run longer than the window only the last W tokens stay
-    live[i] = r < static_cast<int64_t>(n) * p.Hkv && r >= static_cast<int64_t>(n - p.W) * p.Hkv;
-    if (live[i]) raw[i].load(x + r * D);
+    const int r = at.r0 + i * R::kStep;
+    live[i] = r < end && r >= skip * p.Hkv;
+    if (live[i]) raw[i].load(x + static_cast<int64_t>(r) * D);
     else raw[i].clear();
   }
   uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * 16;
   uint8_t* exps = (is_v ? p.exp[1] : p.exp[0]) + static_cast<int64_t>(b) * p.Hkv * p.W;
-  const int slot0 = static_cast<int>(pos % p.W);
+  const int slot0 = static_cast<int>((pos + skip) % p.W);
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
     float v[16];
@@ -99,9 +100,9 @@ __global__ void __launch_bounds__(kRunThreads) kv8_write_kernel(const __grid_con
 #pragma unroll
     for (int off = R::kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
     if (live[i]) {
-      const int64_t r = at.r0 + i * R::kStep;
-      const int t = static_cast<int>(r / p.Hkv), h = static_cast<int>(r - static_cast<int64_t>(t) * p.Hkv);
-      const int64_t slot = (static_cast<int64_t>(slot0) + t) % p.W;
+      int h;
+      const int t = p.heads.divmod(at.r0 + i * R::kStep, h) - skip;  // < W
+      const int64_t slot = t < p.W - slot0 ? slot0 + t : t - (p.W - slot0);
       const int e = kv8_exponent(a);
       const uint2 lo = quantise8(v, e), hi = quantise8(v + 8, e);
       *reinterpret_cast<uint4*>(x8 + (slot * p.Hkv + h) * D) = make_uint4(lo.x, lo.y, hi.x, hi.y);
@@ -117,8 +118,8 @@ __global__ void __launch_bounds__(kRunThreads) kv8_read_kernel(const __grid_cons
   const int b = blockIdx.y;
   const bool is_v = blockIdx.z;
   const long long pos = p.pos[b];
-  const int64_t rows = static_cast<int64_t>(run_length(p, b)) * p.Hkv;
-  if (pos < 0) return;
+  const int rows = run_length(p, b) * p.Hkv;
+  if (pos < 0 || at.r0 >= rows) return;
   const uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * 16;
   const uint8_t* exps = (is_v ? p.exp[1] : p.exp[0]) + static_cast<int64_t>(b) * p.Hkv * p.W;
   const int slot0 = static_cast<int>(pos % p.W);
@@ -126,10 +127,11 @@ __global__ void __launch_bounds__(kRunThreads) kv8_read_kernel(const __grid_cons
   int e[kRunRows];
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
-    const int64_t r = at.r0 + i * R::kStep;
+    const int r = at.r0 + i * R::kStep;
     if (r < rows) {
-      const int t = static_cast<int>(r / p.Hkv), h = static_cast<int>(r - static_cast<int64_t>(t) * p.Hkv);
-      const int64_t slot = (static_cast<int64_t>(slot0) + t) % p.W;
+      int h;
+      int64_t slot = slot0 + static_cast<int64_t>(p.heads.divmod(r, h));
+      if (slot >= p.W) slot %= p.W;
       q[i] = *reinterpret_cast<const uint4*>(x8 + (slot * p.Hkv + h) * D);
       e[i] = exps[h * static_cast<int64_t>(p.W) + slot] - 127;
     }
@@ -137,13 +139,14 @@ __global__ void __launch_bounds__(kRunThreads) kv8_read_kernel(const __grid_cons
   T* x = static_cast<T*>(is_v ? p.x[1] : p.x[0]) + static_cast<int64_t>(b) * p.T * p.Hkv * D + at.part * 16;
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
-    const int64_t r = at.r0 + i * R::kStep;
+    const int r = at.r0 + i * R::kStep;
     if (r < rows) {
+      T* y = x + static_cast<int64_t>(r) * D;
       float v[8];
       dequantise8(make_uint2(q[i].x, q[i].y), e[i], v);
-      store8(x + r * D, v);
+      store8(y, v);
       dequantise8(make_uint2(q[i].z, q[i].w), e[i], v);
-      store8(x + r * D + 8, v);
+      store8(y + 8, v);
     }
   }
 }
@@ -176,7 +179,7 @@ swa_status run(void* k, void* v, void* k8, uint8_t* k_exp, void* v8, uint8_t* v_
   if (B < 0 || T < 0 || W < 1 || Hkv < 1 || D < 1) return SWA_ERR_ARG;
   if (dtype != SWA_F32 && dtype != SWA_BF16) return SWA_ERR_ARG;
   if (D != 32 && D != 64 && D != 128) return SWA_ERR_UNSUPPORTED;
-  if (B > 65535 || static_cast<int64_t>(T) * Hkv > (1ll << 33)) return SWA_ERR_SHAPE;
+  if (B > 65535 || static_cast<int64_t>(T) * Hkv >= (1ll << 30)) return SWA_ERR_SHAPE;
   if (B == 0 || T == 0) return SWA_OK;
   if (!k || !v || !k8 || !k_exp || !v8 || !v_exp || !pos) return SWA_ERR_ARG;
   if (!al16(k) || !al16(v) || !al16(k8) || !al16(v8) || (reinterpret_cast<uintptr_t>(pos) & 7u) ||
@@ -184,7 +187,7 @@ swa_status run(void* k, void* v, void* k8, uint8_t* k_exp, void* v8, uint8_t* v_
     return SWA_ERR_ARG;
   int* err = nullptr;
   if (const int ds = device_ready_status(&err)) return static_cast<swa_status>(ds);
-  RunParams p{{k, v}, {static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8)}, {k_exp, v_exp}, pos, count, B, T, W, Hkv};
+  RunParams p{{k, v}, {static_cast<uint8_t*>(k8), static_cast<uint8_t*>(v8)}, {k_exp, v_exp}, pos, count, B, T, W, Hkv, FastDiv(Hkv)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == SWA_BF16 ? launch_run_d<kWrite, __nv_bfloat16>(p, D, st)
                                           : launch_run_d<kWrite, float>(p, D, st);

@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "../../include/swa.h"
+#include "fastdiv.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -39,10 +40,10 @@ struct RopeParams {
   const int* pos;           // [tokens, axes]
   int64_t tokens;
   int64_t x_row, y_row;     // bytes between token rows
-  int pieces;               // 16-byte pieces of a token's heads
-  int head_pieces;          // ... of one head
+  FastDiv pieces;           // 16-byte pieces of a token's heads
+  FastDiv head_pieces;      // ... of one head
   int pairs, axes;          // pairs that turn, of all axes together
-  int half;                 // head_dim / 2
+  FastDiv half;             // head_dim / 2
   int tokens_per_block;
   int inverse;
   int first[kRopeMaxAxes];  // first pair of each axis
@@ -87,20 +88,29 @@ __global__ void __launch_bounds__(kRopeThreads) rope_nd_kernel(const __grid_cons
   __shared__ __align__(16) float2 table[kRopeTablePairs];
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tokens_per_block;
   const int n_tok = static_cast<int>(p.tokens - tok0 < p.tokens_per_block ? p.tokens - tok0 : p.tokens_per_block);
-  const int n = n_tok * p.pieces;
+  const int n = n_tok * static_cast<int>(p.pieces.d), half = static_cast<int>(p.half.d);
   const uint8_t* x = p.x + tok0 * p.x_row;
   uint8_t* y = p.y + tok0 * p.y_row;
+  auto get = [&](int i) {
+    int c;
+    const int tk = p.pieces.divmod(i, c);
+    return *reinterpret_cast<const uint4*>(x + tk * p.x_row + c * 16);
+  };
+  auto put = [&](int i, uint4 u) {
+    int c, part;
+    const int tk = p.pieces.divmod(i, c);
+    p.head_pieces.divmod(c, part);
+    *reinterpret_cast<uint4*>(y + tk * p.y_row + c * 16) = rotate_piece<T>(u, table + tk * half + part * kPairs);
+  };
   uint4 v[kRopeAhead];
 #pragma unroll
   for (int k = 0; k < kRopeAhead; ++k) {
     const int i = threadIdx.x + k * kRopeThreads;
-    if (i < n) {
-      const int tk = i / p.pieces;
-      v[k] = *reinterpret_cast<const uint4*>(x + tk * p.x_row + (i - tk * p.pieces) * 16);
-    }
+    if (i < n) v[k] = get(i);
   }
-  for (int i = threadIdx.x; i < n_tok * p.half; i += kRopeThreads) {
-    const int tk = i / p.half, j = i - tk * p.half;
+  for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
+    int j;
+    const int tk = p.half.divmod(i, j);
     float2 cs = make_float2(1.f, 0.f);  // a pair behind the axes' stays as it is
     if (j < p.pairs) {
       int a = 0;
@@ -112,20 +122,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_nd_kernel(const __grid_cons
     table[i] = cs;
   }
   __syncthreads();
-  auto put = [&](int i, uint4 u) {
-    const int tk = i / p.pieces, c = i - tk * p.pieces;
-    u = rotate_piece<T>(u, table + tk * p.half + (c % p.head_pieces) * kPairs);
-    *reinterpret_cast<uint4*>(y + tk * p.y_row + c * 16) = u;
-  };
 #pragma unroll
   for (int k = 0; k < kRopeAhead; ++k) {
     const int i = threadIdx.x + k * kRopeThreads;
     if (i < n) put(i, v[k]);
   }
-  for (int i = threadIdx.x + kRopeAhead * kRopeThreads; i < n; i += kRopeThreads) {
-    const int tk = i / p.pieces;
-    put(i, *reinterpret_cast<const uint4*>(x + tk * p.x_row + (i - tk * p.pieces) * 16));
-  }
+  for (int i = threadIdx.x + kRopeAhead * kRopeThreads; i < n; i += kRopeThreads) put(i, get(i));
 }
 
 }  // namespace
@@ -164,18 +166,19 @@ extern "C" swa_status swa_rope_nd(const void* x, void* y, const int32_t* pos, lo
   p.tokens = tokens;
   p.x_row = x_row_stride * esize;
   p.y_row = y_row_stride * esize;
-  p.pieces = static_cast<int>(row * esize / 16);
-  p.head_pieces = head_dim * esize / 16;
+  const int pieces = static_cast<int>(row * esize / 16);
+  p.pieces = FastDiv(pieces);
+  p.head_pieces = FastDiv(head_dim * esize / 16);
   p.pairs = n;
   p.axes = axes;
-  p.half = head_dim / 2;
+  p.half = FastDiv(head_dim / 2);
   p.inverse = inverse != 0;
   // whole tokens for about four pieces a thread, within the table, and not so many
   // that SMs are left without a block
-  const int64_t fill = (kRopeAhead * kRopeThreads + p.pieces - 1) / p.pieces;
+  const int64_t fill = (kRopeAhead * kRopeThreads + pieces - 1) / pieces;
   const int64_t spread = (tokens + 2 * device_sms() - 1) / (2 * device_sms());
   p.tokens_per_block = static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>({fill, spread, kRopeTablePairs / p.half})));
+      std::max<int64_t>(1, std::min<int64_t>({fill, spread, kRopeTablePairs / (head_dim / 2)})));
   const int64_t blocks = (tokens + p.tokens_per_block - 1) / p.tokens_per_block;
   if (blocks > 0x7fffffffll) return SWA_ERR_SHAPE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
