@@ -4,9 +4,10 @@
 // Every sequence b has its own position pos[b] (in device memory, so that a
 // captured step can be replayed as the positions advance) and so its own number
 // of keys, cut into tiles of 128.  An item is one (sequence, KV head, group of up to 8
-// of its query heads).  The tiles of all sequences, in order, form one line, in
-// which every sequence begins with kSeqStart tiles' worth of nothing (what changing
-// over to it costs); team c of C takes the part [c T / C, (c + 1) T / C) of its T places.
+// of its query heads).  The keys of all sequences, in order and 32 to a place, form one
+// line, in which every sequence begins with kSeqStart empty places (what changing
+// over to it costs); team c of C takes the part [c T / C, (c + 1) T / C) of its T places,
+// to whole tiles.
 // A team is one CTA per item of a sequence, and its CTAs walk the same tiles side by
 // side: a token's KV heads lie next to one another in a cache, so the team reads
 // whole rows of memory together.  (With the heads' CTAs at different places of the
@@ -29,7 +30,12 @@ namespace swa {
 constexpr int kSeqKeys = 128;     // keys of a tile
 constexpr int kSeqRows = 8;       // query heads of an item
 constexpr int kSeqMaxCtas = 640;  // CTAs of a launch (or one team, if that is more)
-constexpr int kSeqStart = 2;      // of 0, 1 and 2, 2 ran 33 sequences of 82 to 8192 tokens fastest (43.9, 42.8, 41.3 us)
+constexpr int kSeqPlace = 32;      // keys of a place
+#ifndef SWA_SEQ_START
+#define SWA_SEQ_START 8
+#endif
+constexpr int kSeqStart = SWA_SEQ_START;
+constexpr int kSeqTile = kSeqKeys / kSeqPlace;  // places of a tile
 constexpr int kSeqCols = 16;      // query columns of the tensor-core products
 constexpr int kSeqMaxSplits = 64; // pieces of a shared prefix
 
@@ -60,6 +66,7 @@ struct SeqParams {
   int* err;
   int W, B, Hq, Hkv, G;   // G query heads per KV head
   int groups, items;      // groups of 8 heads per KV head; items per sequence = Hkv * groups
+  int score_ctas;         // CTAs of a cluster that scores a row's blocks
   int block, n_select, n_first, n_last, n_blocks;  // block-sparse (block = 0: all keys)
   int N, splits;          // shared prefix
   int teams, ctas;        // ctas = teams * items
@@ -74,13 +81,14 @@ SWA_DEV int seq_tokens(const SeqParams& p, int b) {
   return pos < 0 ? 0 : (pos >= p.W - 1 ? p.W : static_cast<int>(pos) + 1);
 }
 
-// tiles of each item of sequence b
-SWA_DEV int seq_tiles(const SeqParams& p, int b) {
+// places and tiles of each item of sequence b
+SWA_DEV int seq_places(const SeqParams& p, int b) {
   const int n = seq_tokens(p, b);
-  if (p.block == 0) return (n + kSeqKeys - 1) / kSeqKeys;
+  if (p.block == 0) return (n + kSeqPlace - 1) / kSeqPlace;
   const int blocks = min((n + p.block - 1) / p.block, p.n_select);
-  return (blocks * p.block + kSeqKeys - 1) / kSeqKeys;
+  return (blocks * p.block + kSeqPlace - 1) / kSeqPlace;
 }
+SWA_DEV int seq_tiles(const SeqParams& p, int b) { return (seq_places(p, b) + kSeqTile - 1) / kSeqTile; }
 
 // team that owns place t of the line of T >= teams: the c with c T / C <= t < (c + 1) T / C
 SWA_DEV int seq_owner(int64_t t, int64_t T, int teams) { return static_cast<int>(((t + 1) * teams - 1) / T); }
@@ -126,7 +134,7 @@ struct SeqWalk {
 // ``lane`` returns its D / 32 elements of sum_i 2^(m_i - M) O_i, and L = sum_i 2^(m_i - M) l_i.
 // A lane holds one piece's weight, and the outputs are added with independent loads
 // (from L2: other SMs have just written them).
-template <int D, typename O, typename ML>
+template <int D, int Unroll, typename O, typename ML>
 SWA_DEV void merge_pieces(int n, int stride, int first, int lane, O o_of, ML ml_of, float* acc, float& M, float& L) {
   constexpr int E = D / 32;
   M = -INFINITY;
@@ -151,7 +159,7 @@ SWA_DEV void merge_pieces(int n, int stride, int first, int lane, O o_of, ML ml_
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= keep;
     const int k1 = min(32, (n - i0 + stride - 1) / stride);
-#pragma unroll 4
+#pragma unroll Unroll
     for (int k = 0; k < k1; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
       const float* o = o_of(i0 + k * stride) + lane * E;

@@ -3,8 +3,8 @@
 // (swa_decode_prefix) and over blocks that a score selects (swa_decode_sparse).
 //
 // One step is a chain of kernels, each a programmatic dependent launch behind the
-// one before: the new token enters the cache and the work is divided (seq.cuh);
-// block-sparse: scores and selection; the prefix's pieces; the attention over the
+// one before: the new token enters the cache and the work is divided (seq.cuh), and
+// block-sparse the blocks are scored and selected; the prefix's pieces; the attention over the
 // caches; with a prefix, the merge.
 #include <cuda_runtime.h>
 
@@ -59,20 +59,22 @@ SWA_DEV void seq_divide(const SeqParams& p) {
   int T = 0, tiles = 0, n;
   for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
     const int b = b0 + threadIdx.x;
-    const int mine = b < p.B ? seq_tiles(p, b) : 0;
+    const int mine = b < p.B ? seq_places(p, b) : 0;
     int2 before;
     before.x = T + block_sum(mine > 0 ? mine + kSeqStart : 0, n);
     T += n;
-    before.y = tiles + block_sum(mine, n);
+    before.y = tiles + block_sum((mine + kSeqTile - 1) / kSeqTile, n);
     tiles += n;
     if (b < p.B) p.own[b] = before;
   }
   __syncthreads();
-  const int teams = min(p.teams, T);  // no part is empty
+  // no part is smaller than a tile, so that the pieces of a cut item are those of teams
+  // that follow one another
+  const int teams = min(p.teams, max(1, T / kSeqTile));
   for (int c = threadIdx.x; c < p.teams; c += kPrepThreads) {
     int4 s = make_int4(0, 0, 0, 0);
-    if (c < teams) {
-      // the sequence that holds place t < T, and the tiles in front of t
+    if (c < teams && T > 0) {
+      // the sequence that holds place t < T, and the tiles that begin in front of t
       auto find = [&](int t, int& lo) {
         lo = 0;  // the last b whose places begin at t or before it
         for (int hi = p.B; hi - lo > 1;) {
@@ -80,7 +82,7 @@ SWA_DEV void seq_divide(const SeqParams& p) {
           if (p.own[mid].x <= t) lo = mid;
           else hi = mid;
         }
-        return p.own[lo].y + max(0, t - p.own[lo].x - kSeqStart);
+        return p.own[lo].y + max(0, t - p.own[lo].x - kSeqStart) / kSeqTile;
       };
       const int t = static_cast<int>(static_cast<int64_t>(T) * c / teams);
       const int end = static_cast<int>(static_cast<int64_t>(T) * (c + 1) / teams);
@@ -93,10 +95,11 @@ SWA_DEV void seq_divide(const SeqParams& p) {
   }
   __syncthreads();
   for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
-    const int of = seq_tiles(p, b), t = p.own[b].x + kSeqStart;
+    // tile j is the last team's that begins at place 4 j + 3 of the sequence or before it
+    const int of = seq_places(p, b), t = p.own[b].x + kSeqStart;
     int2 s = make_int2(0, 0);
     if (of > 0) {
-      s.x = seq_owner(t, T, teams);
+      s.x = seq_owner(t + min(kSeqTile, of) - 1, T, teams);
       s.y = seq_owner(t + of - 1, T, teams) - s.x + 1;
     }
     p.own[b] = s;
@@ -233,10 +236,10 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const SeqParams p) {
 // as the definition orders them and only ties go to the lower index: in 32 bits two
 // near scores may change places, and with them what the step attends to.
 //
-// Bound: the bounds' bytes.  A CTA takes 64 blocks of one (sequence, KV head); lanes
-// hold 16 bytes of a row each, and their part of up and down in registers.  The
-// CTA that holds the token's block first renews its bounds from all its valid keys
-// (the slot's old key may have been one of the extremes).
+// Bound: the bounds' bytes.  The CTAs of a cluster take 64 blocks of one (sequence, KV
+// head) in turn, lanes 16 bytes of a row each; the CTA that has the token's
+// block first renews its bounds from all its valid keys (the slot's old key may have
+// been one of the extremes).  When all have finished, the first CTA selects.
 SWA_DEV uint64_t sortable(double x) {
   if (isnan(x)) return 0;  // behind every number
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));  // -0 as +0
@@ -244,7 +247,8 @@ SWA_DEV uint64_t sortable(double x) {
 }
 
 constexpr int kScoreThreads = kPrepThreads;
-constexpr int kScoreBlocks = 64;  // cache blocks of a CTA
+constexpr int kScoreBlocks = 64;  // cache blocks of a CTA at a time
+constexpr int kScoreCtas = 8;     // CTAs of a row at most (a cluster)
 
 // 16 bytes of a row in 32 bits
 template <typename T>
@@ -290,30 +294,164 @@ SWA_DEV double dot_piece(uint4 v, const double* w) {
   return s;
 }
 
+// ---- selection
+// The n_select greatest scores of a row, ties to the lower index, their indices in
+// ascending order.  Forced blocks (all bits set) are counted first.  Of the others the
+// threshold is found 8 bits at a time from the highest bit in which they differ (a
+// histogram of the scores that agree with the bits found so far, summed from its upper
+// end by all threads), until a bin is wanted whole; then one ordered pass writes what is
+// above the threshold and the first of what equals it.
+constexpr int kSelKeep = 2048;  // scores kept in shared memory
+
+struct SelectMem {
+  uint64_t keep[kSelKeep];
+  int hist[256];
+  int wsum[2][kPrepWarps];
+  uint64_t bits[2][kPrepWarps];
+  int bin, want, whole;
+};
+
+SWA_DEV uint64_t warp_or(uint64_t v) {
+  return static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(v >> 32))) << 32 |
+         __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(v));
+}
+
+SWA_DEV void select_blocks(const uint64_t* score, int used, int take, int* sel, SelectMem& sm) {
+  constexpr uint64_t kForced = ~0ull;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // which bits are set in some and in all of the scores, and how many are forced
+  uint64_t some = 0, none = 0;
+  int forced = 0;
+  for (int j = threadIdx.x; j < used; j += kScoreThreads) {
+    const uint64_t s = __ldcg(score + j);
+    if (used <= kSelKeep) sm.keep[j] = s;
+    if (s == kForced) {
+      ++forced;
+    } else {
+      some |= s;
+      none |= ~s;
+    }
+  }
+  if (used <= kSelKeep) score = sm.keep;
+  some = warp_or(some);
+  none = warp_or(none);
+  forced = __reduce_add_sync(0xffffffffu, forced);
+  if (lane == 0) {
+    sm.bits[0][warp] = some;
+    sm.bits[1][warp] = none;
+    sm.wsum[0][warp] = forced;
+  }
+  __syncthreads();
+  some = none = 0;
+  forced = 0;
+  for (int w = 0; w < kPrepWarps; ++w) {
+    some |= sm.bits[0][w];
+    none |= sm.bits[1][w];
+    forced += sm.wsum[0][w];
+  }
+  uint64_t found = kForced, mask = ~0ull;  // nothing but the forced ones is wanted
+  int want = forced;
+  if (take > forced) {
+    const uint64_t differ = some & none;
+    const int top = differ ? 63 - __clzll(static_cast<long long>(differ)) : 0;
+    int shift = max(0, top - 7);
+    mask = top == 63 ? 0 : ~0ull << (top + 1);
+    found = some & mask;
+    want = take - forced;  // scores still to be found among those that agree with `found`
+    while (true) {
+      sm.hist[threadIdx.x] = 0;
+      __syncthreads();
+      for (int j = threadIdx.x; j < used; j += kScoreThreads) {
+        const uint64_t s = score[j];
+        if (s != kForced && (s & mask) == found) atomicAdd(&sm.hist[(s >> shift) & 255], 1);
+      }
+      __syncthreads();
+      // thread t: bin 255 - t, the scores in it and in all above it
+      const int mine = sm.hist[255 - threadIdx.x];
+      int sum = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+      }
+      if (lane == 31) sm.wsum[0][warp] = sum;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) sum += sm.wsum[0][w];
+      if (sum >= want && sum - mine < want) {
+        sm.bin = 255 - threadIdx.x;
+        sm.want = want - (sum - mine);
+        sm.whole = sum == want;
+      }
+      __syncthreads();
+      found |= static_cast<uint64_t>(sm.bin) << shift;
+      mask |= 255ull << shift;
+      want = sm.want;
+      // wanted whole: no lower bit decides anything
+      if (sm.whole || shift == 0) break;
+      shift = max(0, shift - 8);
+    }
+  }
+  int above = 0, equal = 0;  // so far, over all threads
+  for (int j0 = 0; j0 < used; j0 += kScoreThreads) {
+    const int j = j0 + threadIdx.x;
+    const uint64_t s = j < used ? score[j] : 0;
+    const bool e = j < used && (s & mask) == found && (s != kForced || found == kForced);
+    const bool a = j < used && !e && (s & mask) >= found;
+    const unsigned ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
+    __syncthreads();  // the sums of the round before are read
+    if (lane == 0) {
+      sm.wsum[0][warp] = __popc(ba);
+      sm.wsum[1][warp] = __popc(be);
+    }
+    __syncthreads();
+    int xa = above + __popc(ba & ((1u << lane) - 1)), xe = equal + __popc(be & ((1u << lane) - 1));
+    for (int w = 0; w < kPrepWarps; ++w) {
+      if (w < warp) {
+        xa += sm.wsum[0][w];
+        xe += sm.wsum[1][w];
+      }
+      above += sm.wsum[0][w];
+      equal += sm.wsum[1][w];
+    }
+    if (a || (e && xe < want)) sel[xa + min(xe, want)] = j;
+  }
+}
+
+// grid: a cluster for the division of the work, then one for each (sequence, KV head)
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
   constexpr int E = 16 / sizeof(T);       // elements of a lane
   constexpr int kLanes = D / E;           // lanes of a row
   constexpr int kRows = kScoreThreads / kLanes;
-  const int chunks = (p.n_blocks + kScoreBlocks - 1) / kScoreBlocks;
-  if (blockIdx.x == 0) {
-    seq_divide(p);
+  __shared__ union {
+    struct {
+      float low[kRows][D], high[kRows][D];
+    } b;
+    SelectMem select;
+  } sm;
+  __shared__ double up[D], down[D];
+  const int ctas = p.score_ctas, rank = blockIdx.x % ctas;
+  const int64_t row = static_cast<int64_t>(blockIdx.x / ctas) - 1;
+  if (row < 0) {
+    if (rank == 0) seq_divide(p);
     return;
   }
-  const int64_t u = blockIdx.x - 1;
-  const int64_t row = u / chunks;  // (b, KV head)
   const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<int64_t>(b) * p.Hkv);
-  const int j0 = static_cast<int>(u - row * chunks) * kScoreBlocks;
   const int n = seq_tokens(p, b);
   const int used = n > 0 ? (n + p.block - 1) / p.block : 0;
-  if (j0 == 0 && threadIdx.x < 32) seq_start_row<T, D>(p, row, n == 0, threadIdx.x);
-  if (j0 >= used) return;
+  const int take = min(used, p.n_select);
+  int* sel = p.selected + row * p.n_select;
+  if (rank == 0) {
+    if (threadIdx.x < 32) seq_start_row<T, D>(p, row, n == 0, threadIdx.x);
+    for (int i = take + threadIdx.x; i < p.n_select; i += kScoreThreads) sel[i] = -1;
+    if (used == take)
+      for (int i = threadIdx.x; i < used; i += kScoreThreads) sel[i] = i;
+  }
+  if (used == 0) return;
   const int slot = static_cast<int>(p.pos[b] % p.W), newest = slot / p.block;
   const int part = threadIdx.x % kLanes, r = threadIdx.x / kLanes;
-  T* bounds = static_cast<T*>(p.bounds) + row * p.n_blocks * 2 * D + part * E;
-  if (newest >= j0 && newest < j0 + kScoreBlocks) {
-    __shared__ float low[kRows][D], high[kRows][D];
+  if (newest / kScoreBlocks % ctas == rank) {
     const T* kn = static_cast<const T*>(p.k_new) + row * D + part * E;
     const T* vn = static_cast<const T*>(p.v_new) + row * D + part * E;
     T* k = static_cast<T*>(p.k_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + part * E;
@@ -339,16 +477,16 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      low[r][part * E + i] = lo[i];
-      high[r][part * E + i] = hi[i];
+      sm.b.low[r][part * E + i] = lo[i];
+      sm.b.high[r][part * E + i] = hi[i];
     }
     __syncthreads();
     if (threadIdx.x < D) {
-      float a = low[0][threadIdx.x], c = high[0][threadIdx.x];
+      float a = sm.b.low[0][threadIdx.x], c = sm.b.high[0][threadIdx.x];
 #pragma unroll
       for (int i = 1; i < kRows; ++i) {
-        a = fminf(a, low[i][threadIdx.x]);
-        c = fmaxf(c, high[i][threadIdx.x]);
+        a = fminf(a, sm.b.low[i][threadIdx.x]);
+        c = fmaxf(c, sm.b.high[i][threadIdx.x]);
       }
       T* o = static_cast<T*>(p.bounds) + (row * p.n_blocks + newest) * 2 * D + threadIdx.x;
       put_f32(o, a);
@@ -356,143 +494,69 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     }
     __syncthreads();
   }
+  if (used == take) return;  // all of them: nothing to choose
   // the rows of a thread's blocks first, so that they are on their way
   constexpr int kIter = kScoreBlocks / kRows;
   constexpr int kAhead = kIter < 4 ? kIter : 4;
+  static_assert(kIter % kAhead == 0, "whole rounds");
+  const T* bounds = static_cast<const T*>(p.bounds) + row * p.n_blocks * 2 * D + part * E;
   uint4 lo[kAhead], hi[kAhead];
-  auto load = [&](int i) {
-    const int j = j0 + i * kRows + r;
-    if (j < used) {
-      const uint4* x = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(j) * 2 * D);
-      lo[i % kAhead] = x[0];
-      hi[i % kAhead] = x[D / E];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * kRows + r;
+      if (j < used) {
+        const uint4* x = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(j) * 2 * D);
+        lo[i] = x[0];
+        hi[i] = x[D / E];
+      }
     }
   };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(i);
-  double up[E], down[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) up[i] = down[i] = 0.0;
-  const T* q = static_cast<const T*>(p.q) + row * p.G * D + part * E;
-  for (int g0 = 0; g0 < p.G; g0 += 4) {
-    float x[4][E];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) load16(q + min(g0 + g, p.G - 1) * D, x[g]);
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      if (g0 + g < p.G)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          // a NaN fails both comparisons and goes to both sums
-          up[i] += x[g][i] < 0.f ? 0.0 : static_cast<double>(x[g][i]);
-          down[i] += x[g][i] > 0.f ? 0.0 : static_cast<double>(x[g][i]);
-        }
-  }
-  // all threads take part in the sums over a row's lanes, with or without a block of their own
-#pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    if (j0 + i * kRows >= used) break;
-    const int j = j0 + i * kRows + r;
-    double s = 0.0;
-    if (j < used) s = dot_piece<T>(lo[i % kAhead], down) + dot_piece<T>(hi[i % kAhead], up);
-    if (i + kAhead < kIter) load(i + kAhead);
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const int back = newest >= j ? newest - j : newest - j + used;
-    if (part == 0 && j < used)
-      p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last) ? ~0ull : sortable(s);
-  }
-}
-
-// ---------------------------------------------------------------- selection
-// The n_select greatest scores of a row, ties to the lower index, their indices in
-// ascending order: the threshold is found a byte at a time from the top (a histogram
-// of the scores that agree with the bytes found so far, summed from its upper end by
-// all threads), until a bin is wanted whole; then one ordered pass writes what is above
-// the threshold and the first of what equals it.
-constexpr int kSelThreads = 256;
-constexpr int kSelKeep = 2048;  // scores kept in shared memory
-
-__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const __grid_constant__ SeqParams p) {
-  griddep_launch_dependents();
-  __shared__ uint64_t keep[kSelKeep];
-  __shared__ int hist[256];
-  __shared__ int wsum[2][kSelThreads / 32];
-  __shared__ int s_bin, s_want, s_whole;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x;
-  const int b = static_cast<int>(row / p.Hkv);
-  const int n = seq_tokens(p, b);
-  const int used = n > 0 ? (n + p.block - 1) / p.block : 0;
-  int* sel = p.selected + row * p.n_select;
-  const int take = min(used, p.n_select);
-  griddep_wait();  // the scores; and an earlier step may still read the selection
-  for (int i = take + threadIdx.x; i < p.n_select; i += kSelThreads) sel[i] = -1;
-  if (used <= p.n_select) {
-    for (int i = threadIdx.x; i < used; i += kSelThreads) sel[i] = i;
-    return;
-  }
-  const uint64_t* score = p.score + row * p.n_blocks;
-  if (used <= kSelKeep) {
-    for (int j = threadIdx.x; j < used; j += kSelThreads) keep[j] = score[j];
-    score = keep;
-    __syncthreads();
-  }
-  uint64_t found = 0, mask = 0;
-  int want = take;  // scores still to be found among those that agree with `found`
-  for (int shift = 56; shift >= 0; shift -= 8) {
-    hist[threadIdx.x] = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < used; j += kSelThreads) {
-      const uint64_t s = score[j];
-      if ((s & mask) == found) atomicAdd(&hist[(s >> shift) & 255], 1);
+  load(rank * kScoreBlocks);
+  if (threadIdx.x < D) {
+    const T* q = static_cast<const T*>(p.q) + row * p.G * D + threadIdx.x;
+    double u = 0.0, d = 0.0;
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g) {
+      const float x = to_f32(q[g * D]);
+      // a NaN fails both comparisons and goes to both sums
+      u += x < 0.f ? 0.0 : static_cast<double>(x);
+      d += x > 0.f ? 0.0 : static_cast<double>(x);
     }
-    __syncthreads();
-    // thread t: bin 255 - t, the scores in it and in all above it
-    const int mine = hist[255 - threadIdx.x];
-    int sum = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, sum, off);
-      if (lane >= off) sum += y;
-    }
-    if (lane == 31) wsum[0][warp] = sum;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) sum += wsum[0][w];
-    if (sum >= want && sum - mine < want) {
-      s_bin = 255 - threadIdx.x;
-      s_want = want - (sum - mine);
-      s_whole = sum == want;
-    }
-    __syncthreads();
-    found |= static_cast<uint64_t>(s_bin) << shift;
-    mask |= 255ull << shift;
-    want = s_want;
-    if (s_whole) break;  // the bin is wanted whole: no byte below it decides anything
+    up[threadIdx.x] = u;
+    down[threadIdx.x] = d;
   }
-  int above = 0, equal = 0;  // so far, over all threads
-  for (int j0 = 0; j0 < used; j0 += kSelThreads) {
-    const int j = j0 + threadIdx.x;
-    const uint64_t s = j < used ? score[j] & mask : 0;
-    const bool a = j < used && s > found, e = j < used && s == found;
-    const unsigned ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
-    __syncthreads();  // the sums of the round before are read
-    if (lane == 0) {
-      wsum[0][warp] = __popc(ba);
-      wsum[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    int xa = above + __popc(ba & ((1u << lane) - 1)), xe = equal + __popc(be & ((1u << lane) - 1));
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) {
-        xa += wsum[0][w];
-        xe += wsum[1][w];
+  __syncthreads();
+  for (int j0 = rank * kScoreBlocks; j0 < used; j0 += ctas * kScoreBlocks) {
+#pragma unroll
+    for (int i0 = 0; i0 < kIter; i0 += kAhead) {
+      double s[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        s[i] = 0.0;
+        if (j0 + (i0 + i) * kRows + r < used)
+          s[i] = dot_piece<T>(lo[i], down + part * E) + dot_piece<T>(hi[i], up + part * E);
       }
-      above += wsum[0][w];
-      equal += wsum[1][w];
+      load(i0 + kAhead < kIter ? j0 + (i0 + kAhead) * kRows : j0 + ctas * kScoreBlocks);
+      // all threads take part in the sums over a row's lanes, with or without a block
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+        const int j = j0 + (i0 + i) * kRows + r;
+        const int back = newest >= j ? newest - j : newest - j + used;
+        if (part == 0 && j < used)
+          p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last) ? ~0ull : sortable(s[i]);
+      }
     }
-    if (a || (e && xe < want)) sel[xa + min(xe, want)] = j;
   }
+  if (ctas > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+  } else {
+    __syncthreads();
+  }
+  select_blocks(p.score + row * p.n_blocks, used, take, sel, sm.select);
 }
 
 // ---------------------------------------------------------------- attention on CUDA cores
@@ -708,7 +772,7 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
     for (int h = threadIdx.x >> 5; h < rows; h += kSimtThreads / 32) {
       const SeqPieces at{p, b, walk.item, h, own};
       float acc[D / 32], M, L;
-      merge_pieces<D>(
+      merge_pieces<D, 4>(
           own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },
           [&](int k) { return p.part_ml + at.at(k) * 2; }, acc, M, L);
       T* out = static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.Hq + kvh * p.G + g0 + h) * D + lane * (D / 32);
@@ -776,7 +840,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const __grid_constant
   const SeqPieces at{p, b, kvh * p.groups + g / kSeqRows, g % kSeqRows, own};
   auto prefix = [&](int i) { return static_cast<int64_t>(i - pieces) * p.B * p.Hq + u; };
   float acc[E], M, L;
-  merge_pieces<D>(
+  merge_pieces<D, 8>(
       pieces ? pieces + p.splits : 0, p.merge_warps, wi, lane,
       [&](int i) { return i < pieces ? p.part_o + at.at(i) * D : p.pre_o + prefix(i) * D; },
       [&](int i) { return i < pieces ? p.part_ml + at.at(i) * 2 : p.pre_ml + prefix(i) * 2; }, acc, M, L);
@@ -877,7 +941,7 @@ swa_status seq_sizes(SeqParams& p, int D, int dtype) {
   p.part_rows = std::min(p.G, kSeqRows);
   if (p.Hq > 65535 ||
       static_cast<int64_t>(p.B) * p.items > 0x3fffffffll || static_cast<int64_t>(p.B) * p.Hq > (1ll << 26) ||
-      static_cast<int64_t>(p.B) * (p.W / kSeqKeys + 2 + kSeqStart) > 0x7fffffffll ||
+      static_cast<int64_t>(p.B) * (p.W / kSeqPlace + 2 + kSeqStart) > 0x7fffffffll ||
       static_cast<int64_t>(p.W) * p.Hkv * D > (1ll << 37))
     return SWA_ERR_SHAPE;
   p.splits = prefix_pieces(p, dtype == SWA_BF16);
@@ -909,12 +973,19 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
         <<<static_cast<unsigned>(1 + (jobs + kPrepWarps - 1) / kPrepWarps), kPrepThreads, 0, st>>>(p);
     e = cudaGetLastError();
   } else if constexpr (KIND == SEQ_PLAIN) {
-    const int64_t chunks = cdiv(p.n_blocks, kScoreBlocks);
-    block_score_kernel<T, D><<<static_cast<unsigned>(1 + rows * chunks), kScoreThreads, 0, st>>>(p);
-    e = cudaGetLastError();
-    if (e == cudaSuccess)
-      e = launch_after(block_select_kernel, dim3(static_cast<unsigned>(rows)), dim3(kSelThreads), 0, st, p);
-    ++launches;
+    const int chunks = cdiv(p.n_blocks, kScoreBlocks);
+    for (p.score_ctas = 1; p.score_ctas < kScoreCtas && p.score_ctas < chunks;) p.score_ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((1 + rows) * p.score_ctas));
+    cfg.blockDim = dim3(kScoreThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.score_ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, block_score_kernel<T, D>, static_cast<const SeqParams&>(p));
   }
   if constexpr (KIND == SEQ_PLAIN) {
     if (e == cudaSuccess && p.N > 0) {
@@ -942,9 +1013,9 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
   }
   if constexpr (KIND == SEQ_PLAIN) {
     if (e == cudaSuccess && p.N > 0) {
-      // pieces of a row: the prefix's, and its share of the teams; a warp for every four
+      // pieces of a row: the prefix's, and its share of the teams; a warp for every 16
       const int pieces = p.splits + p.teams / p.B + 1;
-      p.merge_warps = pieces <= 4 ? 1 : pieces <= 8 ? 2 : pieces <= 16 ? 4 : 8;
+      p.merge_warps = pieces <= 16 ? 1 : pieces <= 32 ? 2 : pieces <= 64 ? 4 : 8;
       const int64_t heads = static_cast<int64_t>(p.B) * p.Hq;
       const int per = 8 / p.merge_warps;
       e = launch_after(prefix_merge_kernel<T, D>, dim3(static_cast<unsigned>((heads + per - 1) / per)), dim3(256), 0, st,
@@ -1079,8 +1150,7 @@ extern "C" swa_status swa_decode_sparse(const void* q, const void* k_new, const 
   if (const swa_status s = seq_sizes(p, head_dim, dtype)) return s;
   if (!block_size(block)) return SWA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(n_first) + n_last > n_select || n_select > (1 << 20) ||
-      static_cast<int64_t>(B) * Hkv > 65535 ||
-      static_cast<int64_t>(B) * Hkv * (W / block / kScoreBlocks + 2) > 0x7fffffffll)
+      static_cast<int64_t>(B) * Hkv > 65535)
     return SWA_ERR_SHAPE;
   if (B == 0) return SWA_OK;
   if (!bounds || !selected) return SWA_ERR_ARG;

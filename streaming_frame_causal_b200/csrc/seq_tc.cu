@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
             for (int h = quarter; h < p.G; h += 4) {
               const SeqPieces at{p, b, kvh, h, own};
               float acc[D / 32], M, L;
-              merge_pieces<D>(
+              merge_pieces<D, 4>(
                   own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },
                   [&](int k) { return p.part_ml + at.at(k) * 2; }, acc, M, L);
               uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) +
