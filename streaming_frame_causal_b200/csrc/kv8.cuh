@@ -69,20 +69,7 @@ SWA_DEV void store8(__nv_bfloat16* x, const float* v) {
                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// largest magnitude of eight elements (NaN passed over)
-SWA_DEV float amax8(const float* v) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
-  return a;
-}
-
-SWA_DEV uint2 quantise8(const float* v, int e) {
-  const float s = pow2i(-e);
-  return make_uint2(to_e4m3x2(v[0] * s, v[1] * s) | to_e4m3x2(v[2] * s, v[3] * s) << 16,
-                    to_e4m3x2(v[4] * s, v[5] * s) | to_e4m3x2(v[6] * s, v[7] * s) << 16);
-}
-
+// eight stored values times 2^e
 SWA_DEV void dequantise8(uint2 q, int e, float* v) {
   const float s = pow2i(e);
   const uint32_t w[4] = {q.x, q.x >> 16, q.y, q.y >> 16};

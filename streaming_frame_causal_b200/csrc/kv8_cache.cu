@@ -2,15 +2,16 @@
 // they are written (swa_kv8_write) and read back (swa_kv8_read).  The format is
 // kv8.cuh's.
 //
-// Bound: device memory.  A row of D elements belongs to D / 16 neighbouring lanes,
-// 16 elements each (16 bytes of the cache), whose largest magnitude is a few
-// shuffles; a thread loads its part of kRunRows rows before it works on the
-// first.  The cache's slots are the rolling ones, position mod W, so a run may wrap
+// Bound: device memory.  A row of D elements belongs to neighbouring lanes, 16 bytes of
+// the unquantised side each (so that a warp's accesses to it leave no sector half
+// done), whose largest magnitude is a few shuffles; a thread loads its part of
+// kRunRows rows before it works on the first.  The cache's slots are the rolling ones, position mod W, so a run may wrap
 // around its end.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/swa.h"
 #include "fastdiv.cuh"
@@ -36,32 +37,58 @@ SWA_DEV int run_length(const RunParams& p, int b) {
   return p.count ? min(max(p.count[b], 0), p.T) : p.T;
 }
 
-constexpr int kRunRows = 4;  // rows of a thread
+constexpr int kRunRows = 8;  // rows of a thread
 
-// 16 elements as they are stored
+// 16 bytes of a row: kEl elements, as they are stored
 template <typename T>
-struct Raw16 {
-  static constexpr int kWords = sizeof(T);
-  uint4 w[kWords];
-  SWA_DEV void load(const T* x) {
+struct Piece {
+  static constexpr int kEl = 16 / sizeof(T);
+  using Bytes = typename std::conditional<kEl == 8, uint2, uint32_t>::type;  // their 8-bit form
+  SWA_DEV static void widen(uint4 w, float* v) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(x)[i];
+    for (int i = 0; i < kEl; ++i) {
+      if constexpr (kEl == 8) v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+      else v[i] = __uint_as_float(u[i]);
+    }
   }
-  SWA_DEV void clear() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  SWA_DEV static uint4 narrow(const float* v) {
+    if constexpr (kEl == 8)
+      return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                        pack_bf16x2(v[6], v[7]));
+    else
+      return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   }
-  SWA_DEV void widen(float* v) const {
-    const T* x = reinterpret_cast<const T*>(w);
-    load8(x, v);
-    load8(x + 8, v + 8);
+  SWA_DEV static Bytes quantise(const float* v, int e) {
+    const float s = pow2i(-e);
+    auto four = [&](const float* x) {
+      return to_e4m3x2(x[0] * s, x[1] * s) | to_e4m3x2(x[2] * s, x[3] * s) << 16;
+    };
+    if constexpr (kEl == 8) return make_uint2(four(v), four(v + 4));
+    else return four(v);
+  }
+  SWA_DEV static void dequantise(Bytes q, int e, float* v) {
+    const float s = pow2i(e);
+    auto four = [&](uint32_t w, float* x) {
+      const float2 a = from_e4m3x2(w), b = from_e4m3x2(w >> 16);
+      x[0] = a.x * s;
+      x[1] = a.y * s;
+      x[2] = b.x * s;
+      x[3] = b.y * s;
+    };
+    if constexpr (kEl == 8) {
+      four(q.x, v);
+      four(q.y, v + 4);
+    } else {
+      four(q, v);
+    }
   }
 };
 
 // The rows (token, head) of a thread in one sequence's run: r0, r0 + step, ...
-template <int D>
+template <typename T, int D>
 struct RunRows {
-  static constexpr int kLanes = D / 16;
+  static constexpr int kLanes = D / Piece<T>::kEl;
   static constexpr int kStep = kRunThreads / kLanes;
   int r0, part;
   SWA_DEV RunRows()
@@ -71,7 +98,8 @@ struct RunRows {
 // grid: x over the rows of one sequence, y the sequence, z K or V
 template <typename T, int D>
 __global__ void __launch_bounds__(kRunThreads) kv8_write_kernel(const __grid_constant__ RunParams p) {
-  using R = RunRows<D>;
+  using R = RunRows<T, D>;
+  using P = Piece<T>;
   const R at;
   const int b = blockIdx.y;
   const bool is_v = blockIdx.z;
@@ -79,24 +107,24 @@ __global__ void __launch_bounds__(kRunThreads) kv8_write_kernel(const __grid_con
   // of a run longer than the window only the last W tokens stay
   const int end = run_length(p, b) * p.Hkv, skip = max(0, run_length(p, b) - p.W);
   if (pos < 0 || at.r0 - static_cast<int>(threadIdx.x) / R::kLanes >= end) return;
-  const T* x = static_cast<const T*>(is_v ? p.x[1] : p.x[0]) + static_cast<int64_t>(b) * p.T * p.Hkv * D + at.part * 16;
-  Raw16<T> raw[kRunRows];
+  const T* x = static_cast<const T*>(is_v ? p.x[1] : p.x[0]) + static_cast<int64_t>(b) * p.T * p.Hkv * D + at.part * P::kEl;
+  uint4 raw[kRunRows];
   bool live[kRunRows];
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
     const int r = at.r0 + i * R::kStep;
     live[i] = r < end && r >= skip * p.Hkv;
-    if (live[i]) raw[i].load(x + static_cast<int64_t>(r) * D);
-    else raw[i].clear();
+    raw[i] = live[i] ? *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(r) * D) : make_uint4(0, 0, 0, 0);
   }
-  uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * 16;
+  uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * P::kEl;
   uint8_t* exps = (is_v ? p.exp[1] : p.exp[0]) + static_cast<int64_t>(b) * p.Hkv * p.W;
   const int slot0 = static_cast<int>((pos + skip) % p.W);
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
-    float v[16];
-    raw[i].widen(v);
-    float a = fmaxf(amax8(v), amax8(v + 8));
+    float v[P::kEl], a = 0.f;
+    P::widen(raw[i], v);
+#pragma unroll
+    for (int j = 0; j < P::kEl; ++j) a = fmaxf(a, fabsf(v[j]));
 #pragma unroll
     for (int off = R::kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
     if (live[i]) {
@@ -104,8 +132,7 @@ __global__ void __launch_bounds__(kRunThreads) kv8_write_kernel(const __grid_con
       const int t = p.heads.divmod(at.r0 + i * R::kStep, h) - skip;  // < W
       const int64_t slot = t < p.W - slot0 ? slot0 + t : t - (p.W - slot0);
       const int e = kv8_exponent(a);
-      const uint2 lo = quantise8(v, e), hi = quantise8(v + 8, e);
-      *reinterpret_cast<uint4*>(x8 + (slot * p.Hkv + h) * D) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      *reinterpret_cast<typename P::Bytes*>(x8 + (slot * p.Hkv + h) * D) = P::quantise(v, e);
       if (at.part == 0) exps[h * static_cast<int64_t>(p.W) + slot] = static_cast<uint8_t>(e + 127);
     }
   }
@@ -113,17 +140,18 @@ __global__ void __launch_bounds__(kRunThreads) kv8_write_kernel(const __grid_con
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kRunThreads) kv8_read_kernel(const __grid_constant__ RunParams p) {
-  using R = RunRows<D>;
+  using R = RunRows<T, D>;
+  using P = Piece<T>;
   const R at;
   const int b = blockIdx.y;
   const bool is_v = blockIdx.z;
   const long long pos = p.pos[b];
   const int rows = run_length(p, b) * p.Hkv;
   if (pos < 0 || at.r0 >= rows) return;
-  const uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * 16;
+  const uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * P::kEl;
   const uint8_t* exps = (is_v ? p.exp[1] : p.exp[0]) + static_cast<int64_t>(b) * p.Hkv * p.W;
   const int slot0 = static_cast<int>(pos % p.W);
-  uint4 q[kRunRows];
+  typename P::Bytes q[kRunRows];
   int e[kRunRows];
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
@@ -132,28 +160,25 @@ __global__ void __launch_bounds__(kRunThreads) kv8_read_kernel(const __grid_cons
       int h;
       int64_t slot = slot0 + static_cast<int64_t>(p.heads.divmod(r, h));
       if (slot >= p.W) slot %= p.W;
-      q[i] = *reinterpret_cast<const uint4*>(x8 + (slot * p.Hkv + h) * D);
+      q[i] = *reinterpret_cast<const typename P::Bytes*>(x8 + (slot * p.Hkv + h) * D);
       e[i] = exps[h * static_cast<int64_t>(p.W) + slot] - 127;
     }
   }
-  T* x = static_cast<T*>(is_v ? p.x[1] : p.x[0]) + static_cast<int64_t>(b) * p.T * p.Hkv * D + at.part * 16;
+  T* x = static_cast<T*>(is_v ? p.x[1] : p.x[0]) + static_cast<int64_t>(b) * p.T * p.Hkv * D + at.part * P::kEl;
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
     const int r = at.r0 + i * R::kStep;
     if (r < rows) {
-      T* y = x + static_cast<int64_t>(r) * D;
-      float v[8];
-      dequantise8(make_uint2(q[i].x, q[i].y), e[i], v);
-      store8(y, v);
-      dequantise8(make_uint2(q[i].z, q[i].w), e[i], v);
-      store8(y + 8, v);
+      float v[P::kEl];
+      P::dequantise(q[i], e[i], v);
+      *reinterpret_cast<uint4*>(x + static_cast<int64_t>(r) * D) = P::narrow(v);
     }
   }
 }
 
 template <bool kWrite, typename T, int D>
 cudaError_t launch_run(const RunParams& p, cudaStream_t st) {
-  constexpr int kRows = RunRows<D>::kStep * kRunRows;
+  constexpr int kRows = RunRows<T, D>::kStep * kRunRows;
   const int64_t rows = static_cast<int64_t>(p.T) * p.Hkv;
   const dim3 grid(static_cast<unsigned>((rows + kRows - 1) / kRows), p.B, 2);
   if (kWrite)

@@ -231,23 +231,21 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const SeqParams p) {
 // score(j) = sum over the group's query heads and the elements of max(q low_j, q high_j),
 // the sum over the heads of a bound that no key of the block exceeds.  With
 // up = sum_g max(q_g, 0) and down = sum_g min(q_g, 0) it is up . high_j + down . low_j,
-// two products per element whatever the group's size.  The sums are in 64 bits (two
-// more of them than the products of 16-bit values fill), so that blocks are ordered
-// as the definition orders them and only ties go to the lower index: in 32 bits two
-// near scores may change places, and with them what the step attends to.
+// two products per element whatever the group's size.
 //
-// Bound: the bounds' bytes.  The CTAs of a cluster take 64 blocks of one (sequence, KV
+// In 32 bits two near scores may change places, and with them what the step attends
+// to; in 64 the conversions and products of all blocks took 18 us where their bytes take
+// 5 (16 x 8 rows of 512 blocks).  So the scores are formed in 32 bits with a bound d on
+// their error, and only the blocks within 2 d of the last one that would be taken are
+// ordered by scores in 64 bits: one that is further above is among the best by any
+// scores within d, one further below is not.
+//
+// Bound: the bounds' bytes.  The CTAs of a cluster take 128 blocks of one (sequence, KV
 // head) in turn, lanes 16 bytes of a row each; the CTA that has the token's
 // block first renews its bounds from all its valid keys (the slot's old key may have
 // been one of the extremes).  When all have finished, the first CTA selects.
-SWA_DEV uint64_t sortable(double x) {
-  if (isnan(x)) return 0;  // behind every number
-  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));  // -0 as +0
-  return (u >> 63) ? ~u : u | (1ull << 63);
-}
-
 constexpr int kScoreThreads = kPrepThreads;
-constexpr int kScoreBlocks = 64;  // cache blocks of a CTA at a time
+constexpr int kScoreBlocks = 128; // cache blocks of a CTA at a time
 constexpr int kScoreCtas = 8;     // CTAs of a row at most (a cluster)
 
 // 16 bytes of a row in 32 bits
@@ -261,46 +259,28 @@ SWA_DEV void load16(const T* x, float* v) {
   }
 }
 
-// A 32-bit float in 64 bits.  The conversion instruction runs at a quarter of the rate of a
-// 64-bit product, so normal numbers are widened by moving their fields; the rest
-// (zero, subnormal, infinite, NaN) are converted.
-SWA_DEV bool is_normal_bits(uint32_t u) { return (u & 0x7fffffffu) - 0x00800000u < 0x7f000000u; }
-SWA_DEV double widen_bits(uint32_t u) {
-  const uint32_t hi = (((u & 0x7fffffffu) >> 3) + (896u << 20)) | (u & 0x80000000u);
-  return __hiloint2double(static_cast<int>(hi), static_cast<int>(u << 29));
-}
-
-// w . the 16 bytes of a row in v
+// The 16 bytes of a row in v times w, added to s, and the magnitudes added to a.
 template <typename T>
-SWA_DEV double dot_piece(uint4 v, const double* w) {
+SWA_DEV void dot_piece(uint4 v, const float* w, float& s, float& a) {
   constexpr int E = 16 / sizeof(T);
   const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-  uint32_t u[E];
-  bool normal = true;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    if constexpr (sizeof(T) == 2) u[i] = i & 1 ? word[i / 2] & 0xffff0000u : word[i / 2] << 16;
-    else u[i] = word[i];
-    normal &= is_normal_bits(u[i]);
+    float x;
+    if constexpr (sizeof(T) == 2) x = __uint_as_float(i & 1 ? word[i / 2] & 0xffff0000u : word[i / 2] << 16);
+    else x = __uint_as_float(word[i]);
+    s = fmaf(x, w[i], s);
+    a = fmaf(fabsf(x), fabsf(w[i]), a);
   }
-  double s = 0.0;
-  if (normal) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) s = fma(widen_bits(u[i]), w[i], s);
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) s = fma(static_cast<double>(__uint_as_float(u[i])), w[i], s);
-  }
-  return s;
 }
 
+// |score in 32 bits - score| <= kScoreError * (sum of the magnitudes): w is rounded once,
+// and a lane's 8 or 16 products and the sums over 8 to 32 lanes (at most 5 steps) round
+// 22 times in all, 2^-24 each, in score and magnitudes alike
+constexpr float kScoreError = 1.f / (1 << 18);
+
 // ---- selection
-// The n_select greatest scores of a row, ties to the lower index, their indices in
-// ascending order.  Forced blocks (all bits set) are counted first.  Of the others the
-// threshold is found 8 bits at a time from the highest bit in which they differ (a
-// histogram of the scores that agree with the bits found so far, summed from its upper
-// end by all threads), until a bin is wanted whole; then one ordered pass writes what is
-// above the threshold and the first of what equals it.
+// Counts, sums and thresholds are found by all threads of a block together.
 constexpr int kSelKeep = 2048;  // scores kept in shared memory
 
 struct SelectMem {
@@ -308,95 +288,199 @@ struct SelectMem {
   int hist[256];
   int wsum[2][kPrepWarps];
   uint64_t bits[2][kPrepWarps];
-  int bin, want, whole;
+  int bin, want, whole, list;
 };
+
+SWA_DEV uint32_t sortable(float x) {
+  if (isnan(x)) return 0;  // behind every number
+  const uint32_t u = __float_as_uint(x + 0.f);  // -0 as +0
+  return (u >> 31) ? ~u : u | (1u << 31);
+}
+SWA_DEV float unsorted(uint32_t u) { return __uint_as_float((u >> 31) ? u & 0x7fffffffu : ~u); }
 
 SWA_DEV uint64_t warp_or(uint64_t v) {
   return static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(v >> 32))) << 32 |
          __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(v));
 }
 
-SWA_DEV void select_blocks(const uint64_t* score, int used, int take, int* sel, SelectMem& sm) {
-  constexpr uint64_t kForced = ~0ull;
+// The want-th greatest (want >= 1) of the keys key(j) that in(j) admits, at least as many as
+// that: keys that agree with `found` in the bits of `mask` are the ones from which the
+// last `want` have to be taken, and all greater ones belong to the best.  8 bits at a
+// time from the highest in which the keys differ: a histogram of the keys that agree with
+// the bits found so far, summed from its upper end, until a bin is wanted whole.
+template <typename Key, typename In>
+SWA_DEV void find_threshold(int used, int& want, uint64_t& found, uint64_t& mask, SelectMem& sm, Key key, In in) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // which bits are set in some and in all of the scores, and how many are forced
-  uint64_t some = 0, none = 0;
-  int forced = 0;
-  for (int j = threadIdx.x; j < used; j += kScoreThreads) {
-    const uint64_t s = __ldcg(score + j);
-    if (used <= kSelKeep) sm.keep[j] = s;
-    if (s == kForced) {
-      ++forced;
-    } else {
-      some |= s;
-      none |= ~s;
+  uint64_t some = 0, none = 0;  // bits that are set in some, in none of the keys
+  for (int j = threadIdx.x; j < used; j += kScoreThreads)
+    if (in(j)) {
+      some |= key(j);
+      none |= ~key(j);
     }
-  }
-  if (used <= kSelKeep) score = sm.keep;
   some = warp_or(some);
   none = warp_or(none);
-  forced = __reduce_add_sync(0xffffffffu, forced);
   if (lane == 0) {
     sm.bits[0][warp] = some;
     sm.bits[1][warp] = none;
-    sm.wsum[0][warp] = forced;
   }
   __syncthreads();
   some = none = 0;
-  forced = 0;
   for (int w = 0; w < kPrepWarps; ++w) {
     some |= sm.bits[0][w];
     none |= sm.bits[1][w];
-    forced += sm.wsum[0][w];
   }
-  uint64_t found = kForced, mask = ~0ull;  // nothing but the forced ones is wanted
-  int want = forced;
-  if (take > forced) {
-    const uint64_t differ = some & none;
-    const int top = differ ? 63 - __clzll(static_cast<long long>(differ)) : 0;
-    int shift = max(0, top - 7);
-    mask = top == 63 ? 0 : ~0ull << (top + 1);
-    found = some & mask;
-    want = take - forced;  // scores still to be found among those that agree with `found`
-    while (true) {
-      sm.hist[threadIdx.x] = 0;
-      __syncthreads();
-      for (int j = threadIdx.x; j < used; j += kScoreThreads) {
-        const uint64_t s = score[j];
-        if (s != kForced && (s & mask) == found) atomicAdd(&sm.hist[(s >> shift) & 255], 1);
-      }
-      __syncthreads();
-      // thread t: bin 255 - t, the scores in it and in all above it
-      const int mine = sm.hist[255 - threadIdx.x];
-      int sum = mine;
+  const uint64_t differ = some & none;
+  const int top = differ ? 63 - __clzll(static_cast<long long>(differ)) : 0;
+  mask = top == 63 ? 0 : ~0ull << (top + 1);
+  found = some & mask;
+  for (int shift = max(0, top - 7);; shift = max(0, shift - 8)) {
+    sm.hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int j = threadIdx.x; j < used; j += kScoreThreads)
+      if (in(j) && (key(j) & mask) == found) atomicAdd(&sm.hist[(key(j) >> shift) & 255], 1);
+    __syncthreads();
+    // thread t: bin 255 - t, the keys in it and in all above it
+    const int mine = sm.hist[255 - threadIdx.x];
+    int sum = mine;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += y;
-      }
-      if (lane == 31) sm.wsum[0][warp] = sum;
-      __syncthreads();
-      for (int w = 0; w < warp; ++w) sum += sm.wsum[0][w];
-      if (sum >= want && sum - mine < want) {
-        sm.bin = 255 - threadIdx.x;
-        sm.want = want - (sum - mine);
-        sm.whole = sum == want;
-      }
-      __syncthreads();
-      found |= static_cast<uint64_t>(sm.bin) << shift;
-      mask |= 255ull << shift;
-      want = sm.want;
-      // wanted whole: no lower bit decides anything
-      if (sm.whole || shift == 0) break;
-      shift = max(0, shift - 8);
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += y;
     }
+    if (lane == 31) sm.wsum[0][warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += sm.wsum[0][w];
+    if (sum >= want && sum - mine < want) {
+      sm.bin = 255 - threadIdx.x;
+      sm.want = want - (sum - mine);
+      sm.whole = sum == want;
+    }
+    __syncthreads();
+    found |= static_cast<uint64_t>(sm.bin) << shift;
+    mask |= 255ull << shift;
+    want = sm.want;
+    if (sm.whole || shift == 0) break;
   }
+  __syncthreads();
+}
+
+// A block's score in 64 bits, by a warp.
+template <typename T, int D>
+SWA_DEV double exact_score(const T* bounds, const double* up, const double* down, int lane) {
+  double s = 0.0;
+#pragma unroll
+  for (int i = lane; i < D; i += 32) {
+    s = fma(static_cast<double>(to_f32(bounds[D + i])), up[i], s);
+    s = fma(static_cast<double>(to_f32(bounds[i])), down[i], s);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return s;
+}
+
+// The `take` best of `used` > take blocks, in ascending order.  score[j]: the sortable
+// 32-bit score in the upper half (all bits: a forced block) and the bound on its error in
+// the lower; bounds, up, down: what the scores are formed from.
+template <typename T, int D>
+SWA_DEV void select_blocks(uint64_t* score, int used, int take, int* sel, const T* bounds, const double* up,
+                           const double* down, SelectMem& sm) {
+  constexpr uint32_t kForced = ~0u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool kept = used <= kSelKeep;
+  int forced = 0;
+  float err = 0.f;
+  for (int j = threadIdx.x; j < used; j += kScoreThreads) {
+    const uint64_t s = __ldcg(reinterpret_cast<const unsigned long long*>(score + j));
+    if (kept) sm.keep[j] = s;
+    const float e = __uint_as_float(static_cast<uint32_t>(s));
+    if (s >> 32 == kForced) ++forced;
+    else err = e > err || isnan(e) ? e : err;  // a NaN stays
+  }
+  uint64_t* k = kept ? sm.keep : score;
+  if (threadIdx.x == 0) sm.list = 0;
+  forced = __reduce_add_sync(0xffffffffu, forced);
+  // the bits of non-negative floats are ordered as they are, NaN above all
+  const uint32_t top_err = __reduce_max_sync(0xffffffffu, __float_as_uint(err) & 0x7fffffffu);
+  if (lane == 0) {
+    sm.wsum[0][warp] = forced;
+    sm.wsum[1][warp] = static_cast<int>(top_err);
+  }
+  __syncthreads();
+  forced = 0;
+  uint32_t e_bits = 0;
+  for (int w = 0; w < kPrepWarps; ++w) {
+    forced += sm.wsum[0][w];
+    e_bits = max(e_bits, static_cast<uint32_t>(sm.wsum[1][w]));
+  }
+  __syncthreads();
+  const float d = __uint_as_float(e_bits);
+  // Every block becomes kForced (taken), 0 (not taken) or, if only the order in 64 bits can
+  // tell, its score in 64 bits.
+  constexpr uint64_t kTaken = ~0ull;
+  int sure = forced;
+  if (take > forced) {
+    uint64_t found, mask;
+    int want = take - forced;
+    find_threshold(
+        used, want, found, mask, sm, [&](int j) { return k[j] >> 32; }, [&](int j) { return k[j] >> 32 != kForced; });
+    // some score of the bin that the threshold lies in; all of them are within `slack`
+    const float lo = unsorted(static_cast<uint32_t>(found)), hi = unsorted(static_cast<uint32_t>(found | ~mask));
+    const float above = hi + 2.0625f * d, below = lo - 2.0625f * d;  // the sums round, too
+    int mine = 0;
+    for (int j = threadIdx.x; j < used; j += kScoreThreads) {
+      const uint32_t u = static_cast<uint32_t>(k[j] >> 32);
+      const float s = unsorted(u);
+      uint64_t to = 1;  // to be decided
+      if (u == kForced || (u != 0 && s > above)) to = kTaken;
+      else if (u != 0 && s < below) to = 0;
+      mine += to == kTaken;
+      if (to == 1) atomicAdd(&sm.list, 1);
+      k[j] = to;
+    }
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0) sm.wsum[0][warp] = mine;
+    __syncthreads();
+    sure = 0;
+    for (int w = 0; w < kPrepWarps; ++w) sure += sm.wsum[0][w];
+    const bool all = sm.list == take - sure;
+    if (all) {
+      for (int j = threadIdx.x; j < used; j += kScoreThreads)
+        if (k[j] == 1) k[j] = kTaken;
+      sure = take;
+    } else {
+      for (int j0 = warp * 32; j0 < used; j0 += kScoreThreads) {
+        unsigned todo = __ballot_sync(0xffffffffu, j0 + lane < used && k[j0 + lane] == 1);
+        while (todo) {
+          const int j = j0 + __ffs(todo) - 1;
+          todo &= todo - 1;
+          const double s = exact_score<T, D>(bounds + static_cast<int64_t>(j) * 2 * D, up, down, lane);
+          if (lane == 0) {
+            // NaN behind every number, but not with those that are out
+            const uint64_t u = static_cast<uint64_t>(__double_as_longlong(s + 0.0));
+            k[j] = isnan(s) ? 1 : ((u >> 63) ? ~u : u | (1ull << 63));
+          }
+        }
+      }
+    }
+    __syncthreads();
+  } else {
+    for (int j = threadIdx.x; j < used; j += kScoreThreads) k[j] = k[j] >> 32 == kForced ? kTaken : 0;
+    __syncthreads();
+  }
+  uint64_t found = kTaken, mask = kTaken;
+  int want = sure;
+  if (take > sure) {
+    want = take - sure;
+    find_threshold(
+        used, want, found, mask, sm, [&](int j) { return k[j]; }, [&](int j) { return k[j] != 0 && k[j] != kTaken; });
+  }
+  // one ordered pass: what is above the threshold, and the first of what equals it
   int above = 0, equal = 0;  // so far, over all threads
   for (int j0 = 0; j0 < used; j0 += kScoreThreads) {
     const int j = j0 + threadIdx.x;
-    const uint64_t s = j < used ? score[j] : 0;
-    const bool e = j < used && (s & mask) == found && (s != kForced || found == kForced);
-    const bool a = j < used && !e && (s & mask) >= found;
+    const uint64_t s = j < used ? k[j] : 0;
+    const bool e = s != 0 && (s & mask) == found && (s != kTaken || found == kTaken);
+    const bool a = s != 0 && !e && (s == kTaken || (s & mask) > found);
     const unsigned ba = __ballot_sync(0xffffffffu, a), be = __ballot_sync(0xffffffffu, e);
     __syncthreads();  // the sums of the round before are read
     if (lane == 0) {
@@ -419,7 +503,7 @@ SWA_DEV void select_blocks(const uint64_t* score, int used, int take, int* sel, 
 
 // grid: a cluster for the division of the work, then one for each (sequence, KV head)
 template <typename T, int D>
-__global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid_constant__ SeqParams p) {
+__global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
   constexpr int E = 16 / sizeof(T);       // elements of a lane
   constexpr int kLanes = D / E;           // lanes of a row
@@ -431,6 +515,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     SelectMem select;
   } sm;
   __shared__ double up[D], down[D];
+  __shared__ __align__(16) float up32[D], down32[D];
   const int ctas = p.score_ctas, rank = blockIdx.x % ctas;
   const int64_t row = static_cast<int64_t>(blockIdx.x / ctas) - 1;
   if (row < 0) {
@@ -451,24 +536,43 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
   if (used == 0) return;
   const int slot = static_cast<int>(p.pos[b] % p.W), newest = slot / p.block;
   const int part = threadIdx.x % kLanes, r = threadIdx.x / kLanes;
-  if (newest / kScoreBlocks % ctas == rank) {
+  // the rows of a thread's blocks first, so that they are on their way
+  constexpr int kIter = kScoreBlocks / kRows;
+  constexpr int kAhead = kIter < 8 ? kIter : 8;
+  static_assert(kIter % kAhead == 0, "whole rounds");
+  const T* bounds = static_cast<const T*>(p.bounds) + row * p.n_blocks * 2 * D + part * E;
+  uint4 lo[kAhead], hi[kAhead];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * kRows + r;
+      if (j < used) {
+        const uint4* x = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(j) * 2 * D);
+        lo[i] = x[0];
+        hi[i] = x[D / E];
+      }
+    }
+  };
+  if (used > take) load(rank * kScoreBlocks);
+  const bool renews = newest / kScoreBlocks % ctas == rank;
+  if (renews) {
     const T* kn = static_cast<const T*>(p.k_new) + row * D + part * E;
     const T* vn = static_cast<const T*>(p.v_new) + row * D + part * E;
     T* k = static_cast<T*>(p.k_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + part * E;
     T* v = static_cast<T*>(p.v_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + part * E;
     const int64_t step = static_cast<int64_t>(p.Hkv) * D;
-    float lo[E], hi[E], x[E];
+    float least[E], most[E], x[E];
     load16(kn, x);
 #pragma unroll
-    for (int i = 0; i < E; ++i) lo[i] = hi[i] = x[i];
+    for (int i = 0; i < E; ++i) least[i] = most[i] = x[i];
     const int end = min(newest * p.block + p.block, n);
 #pragma unroll 4
     for (int s = newest * p.block + r; s < end; s += kRows) {
       load16(s == slot ? kn : k + s * step, x);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        lo[i] = fminf(lo[i], x[i]);
-        hi[i] = fmaxf(hi[i], x[i]);
+        least[i] = fminf(least[i], x[i]);
+        most[i] = fmaxf(most[i], x[i]);
       }
     }
     if (r == 0) {
@@ -477,8 +581,8 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      sm.b.low[r][part * E + i] = lo[i];
-      sm.b.high[r][part * E + i] = hi[i];
+      sm.b.low[r][part * E + i] = least[i];
+      sm.b.high[r][part * E + i] = most[i];
     }
     __syncthreads();
     if (threadIdx.x < D) {
@@ -495,24 +599,15 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     __syncthreads();
   }
   if (used == take) return;  // all of them: nothing to choose
-  // the rows of a thread's blocks first, so that they are on their way
-  constexpr int kIter = kScoreBlocks / kRows;
-  constexpr int kAhead = kIter < 4 ? kIter : 4;
-  static_assert(kIter % kAhead == 0, "whole rounds");
-  const T* bounds = static_cast<const T*>(p.bounds) + row * p.n_blocks * 2 * D + part * E;
-  uint4 lo[kAhead], hi[kAhead];
-  auto load = [&](int j0) {
+  if (renews) {  // what has just been written was loaded before
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i * kRows + r;
-      if (j < used) {
-        const uint4* x = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(j) * 2 * D);
+    for (int i = 0; i < kAhead; ++i)
+      if (rank * kScoreBlocks + i * kRows + r == newest) {
+        const uint4* x = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(newest) * 2 * D);
         lo[i] = x[0];
         hi[i] = x[D / E];
       }
-    }
-  };
-  load(rank * kScoreBlocks);
+  }
   if (threadIdx.x < D) {
     const T* q = static_cast<const T*>(p.q) + row * p.G * D + threadIdx.x;
     double u = 0.0, d = 0.0;
@@ -525,28 +620,44 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
     }
     up[threadIdx.x] = u;
     down[threadIdx.x] = d;
+    up32[threadIdx.x] = static_cast<float>(u);
+    down32[threadIdx.x] = static_cast<float>(d);
   }
   __syncthreads();
+  float wu[E], wd[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    wu[i] = up32[part * E + i];
+    wd[i] = down32[part * E + i];
+  }
   for (int j0 = rank * kScoreBlocks; j0 < used; j0 += ctas * kScoreBlocks) {
 #pragma unroll
     for (int i0 = 0; i0 < kIter; i0 += kAhead) {
-      double s[kAhead];
+      float s[kAhead], a[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        s[i] = 0.0;
-        if (j0 + (i0 + i) * kRows + r < used)
-          s[i] = dot_piece<T>(lo[i], down + part * E) + dot_piece<T>(hi[i], up + part * E);
+        s[i] = a[i] = 0.f;
+        if (j0 + (i0 + i) * kRows + r < used) {
+          dot_piece<T>(lo[i], wd, s[i], a[i]);
+          dot_piece<T>(hi[i], wu, s[i], a[i]);
+        }
       }
       load(i0 + kAhead < kIter ? j0 + (i0 + kAhead) * kRows : j0 + ctas * kScoreBlocks);
       // all threads take part in the sums over a row's lanes, with or without a block
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
 #pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+        for (int off = kLanes / 2; off > 0; off >>= 1) {
+          s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+          a[i] += __shfl_xor_sync(0xffffffffu, a[i], off);
+        }
         const int j = j0 + (i0 + i) * kRows + r;
         const int back = newest >= j ? newest - j : newest - j + used;
         if (part == 0 && j < used)
-          p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last) ? ~0ull : sortable(s[i]);
+          p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last)
+                                              ? ~0ull
+                                              : static_cast<uint64_t>(sortable(s[i])) << 32 |
+                                                    __float_as_uint(a[i] * kScoreError);
       }
     }
   }
@@ -556,7 +667,8 @@ __global__ void __launch_bounds__(kScoreThreads) block_score_kernel(const __grid
   } else {
     __syncthreads();
   }
-  select_blocks(p.score + row * p.n_blocks, used, take, sel, sm.select);
+  select_blocks<T, D>(p.score + row * p.n_blocks, used, take, sel, static_cast<const T*>(p.bounds) + row * p.n_blocks * 2 * D,
+                      up, down, sm.select);
 }
 
 // ---------------------------------------------------------------- attention on CUDA cores
@@ -571,17 +683,18 @@ template <int D>
 struct SimtPlan {
   static constexpr int kLd = D + 4;
   static constexpr int kTile = kSeqKeys * kLd;
-  static constexpr int kFloats = kTile + kSeqRows * kSeqKeys + kSeqRows * D + 3 * kSeqRows;
+  static constexpr int kFloats = kTile + kSeqRows * kSeqKeys + kSeqRows * D + 3 * kSeqRows + kSeqKeys;
   static constexpr int kSmem = kFloats * 4;
 };
 
-// rows [0, 128) of a tile: row r from slot[r] (behind the keys: zeros), times 2^exp for 8-bit rows
-template <typename T, int D, int KIND, typename Slot>
-SWA_DEV void simt_load(float* tile, const void* rows, int64_t row_elems, const uint8_t* exps, Slot slot_of) {
+// rows [0, 128) of a tile: row r from slot[r] (-1, behind the keys: zeros), times 2^exp for 8-bit rows
+template <typename T, int D, int KIND>
+SWA_DEV void simt_load(float* tile, const void* rows, int64_t row_elems, const uint8_t* exps, const int* slots) {
   constexpr int kParts = D / 8;
+#pragma unroll 8
   for (int i = threadIdx.x; i < kSeqKeys * kParts; i += kSimtThreads) {
     const int r = i / kParts, part = i - r * kParts;
-    const int slot = slot_of(r);
+    const int slot = slots[r];
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (slot >= 0) {
       if constexpr (KIND == SEQ_KV8) {
@@ -601,6 +714,7 @@ template <typename T, int D>
 struct SimtState {
   float acc[kSeqRows];
   float *tile, *w, *q, *m, *l, *alpha;
+  int* slots;  // of the tile's keys
   SWA_DEV void bind(float* smem) {
     tile = smem;
     w = tile + SimtPlan<D>::kTile;
@@ -608,6 +722,7 @@ struct SimtState {
     m = q + kSeqRows * D;
     l = m + kSeqRows;
     alpha = l + kSeqRows;
+    slots = reinterpret_cast<int*>(alpha + kSeqRows);
   }
   // q rows [0, rows) from src, the rest zero
   SWA_DEV void begin(const T* src, int rows) {
@@ -625,8 +740,11 @@ struct SimtState {
   }
   // one tile: keys, then values, loaded by the two functions
   template <typename LoadK, typename LoadV>
-  SWA_DEV void step(float scale_log2, bool valid, LoadK load_k, LoadV load_v) {
+  SWA_DEV void step(float scale_log2, int slot, LoadK load_k, LoadV load_v) {
     const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
+    const bool valid = slot >= 0;
+    slots[r] = slot;
+    __syncthreads();
     load_k();
     __syncthreads();
     float s[kSeqRows];
@@ -736,12 +854,11 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
     const int64_t base = (static_cast<int64_t>(run.b) * p.W * p.Hkv + kvh) * D;
     const int64_t ebase = (static_cast<int64_t>(run.b) * p.Hkv + kvh) * p.W;
     for (int t = run.t0; t < run.t0 + run.tiles; ++t) {
-      auto slot = [&](int r) { return seq_slot(p, run.b, kvh, run.tokens, t, r); };
       auto load = [&](const void* cache, const uint8_t* exps) {
         const uint8_t* rows8 = static_cast<const uint8_t*>(cache) + base * (KIND == SEQ_KV8 ? 1 : sizeof(T));
-        simt_load<T, D, KIND>(st.tile, rows8, row_elems, KIND == SEQ_KV8 ? exps + ebase : nullptr, slot);
+        simt_load<T, D, KIND>(st.tile, rows8, row_elems, KIND == SEQ_KV8 ? exps + ebase : nullptr, st.slots);
       };
-      st.step(p.scale_log2, slot(threadIdx.x) >= 0, [&] { load(p.k_cache, p.k_exp); },
+      st.step(p.scale_log2, seq_slot(p, run.b, kvh, run.tokens, t, threadIdx.x), [&] { load(p.k_cache, p.k_exp); },
               [&] { load(p.v_cache, p.v_exp); });
     }
     st.end(rows, [&](int h, int d, float o, float m, float l) {
@@ -803,12 +920,12 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
   const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits);
   st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
   for (int t = t0; t < t1; ++t) {
-    auto slot = [&](int r) { return t * kSeqKeys + r < p.N ? t * kSeqKeys + r : -1; };
     auto load = [&](const void* x) {
-      simt_load<T, D, SEQ_PLAIN>(st.tile, static_cast<const T*>(x) + kvh * D, static_cast<int64_t>(p.Hkv) * D,
-                                 nullptr, slot);
+      simt_load<T, D, SEQ_PLAIN>(st.tile, static_cast<const T*>(x) + kvh * D, static_cast<int64_t>(p.Hkv) * D, nullptr,
+                                 st.slots);
     };
-    st.step(p.scale_log2, slot(threadIdx.x) >= 0, [&] { load(p.k_prefix); }, [&] { load(p.v_prefix); });
+    const int slot = t * kSeqKeys + static_cast<int>(threadIdx.x);
+    st.step(p.scale_log2, slot < p.N ? slot : -1, [&] { load(p.k_prefix); }, [&] { load(p.v_prefix); });
   }
   st.end(rows, [&](int h, int d, float o, float m, float l) {
     const int64_t at = static_cast<int64_t>(split) * p.B * p.Hq + qrow + h;
@@ -974,7 +1091,9 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
     e = cudaGetLastError();
   } else if constexpr (KIND == SEQ_PLAIN) {
     const int chunks = cdiv(p.n_blocks, kScoreBlocks);
-    for (p.score_ctas = 1; p.score_ctas < kScoreCtas && p.score_ctas < chunks;) p.score_ctas *= 2;
+    // a row's CTAs: as many as let all rows run at a time, two CTAs to an SM
+    for (p.score_ctas = 1; p.score_ctas < kScoreCtas && p.score_ctas < chunks && 2 * p.score_ctas * rows <= 2 * device_sms();)
+      p.score_ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((1 + rows) * p.score_ctas));
     cfg.blockDim = dim3(kScoreThreads);
