@@ -904,15 +904,15 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_constant__ SeqParams p) {
   extern __shared__ __align__(16) float smem[];
   griddep_launch_dependents();
-  griddep_wait();  // the one before may still read the partials of an earlier step
   SimtState<T, D> st;
   st.bind(smem);
   const int kvh = blockIdx.y, split = blockIdx.z;
-  const int64_t rows_all = static_cast<int64_t>(p.B) * p.groups;
   const int64_t rg = blockIdx.x;  // (sequence, group of its heads)
-  if (rg >= rows_all) return;
   const int b = static_cast<int>(rg / p.groups), g0 = static_cast<int>(rg - static_cast<int64_t>(b) * p.groups) * kSeqRows;
-  if (p.pos[b] < 0) return;
+  if (p.pos[b] < 0) {
+    griddep_wait();
+    return;
+  }
   const int rows = min(kSeqRows, p.G - g0);
   const int64_t qrow = static_cast<int64_t>(b) * p.Hq + kvh * p.G + g0;
   const int tiles = (p.N + kSeqKeys - 1) / kSeqKeys;
@@ -935,6 +935,8 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
       p.pre_ml[at * 2 + 1] = l;
     }
   });
+  // the kernels ahead are not needed here, but by those behind, who wait for this one
+  griddep_wait();
 }
 
 // ---------------------------------------------------------------- merge with the prefix
@@ -1106,6 +1108,17 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, block_score_kernel<T, D>, static_cast<const SeqParams&>(p));
   }
+  if constexpr (kTc) {
+    if (e == cudaSuccess) e = launch_seq_tc(p, D, KIND == SEQ_KV8, st);
+  } else if (e == cudaSuccess) {
+    static DeviceOnce once;
+    e = allow_smem(seq_simt_kernel<T, D, KIND>, SimtPlan<D>::kSmem, once);
+    if (e == cudaSuccess)
+      e = launch_after(seq_simt_kernel<T, D, KIND>, dim3(p.ctas), dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
+    ++launches;
+  }
+  // The prefix's kernel needs nothing of the ones ahead of it, so it fills the SMs as
+  // the caches' CTAs leave them.
   if constexpr (KIND == SEQ_PLAIN) {
     if (e == cudaSuccess && p.N > 0) {
       if constexpr (kTc) {
@@ -1120,15 +1133,6 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
         ++launches;
       }
     }
-  }
-  if constexpr (kTc) {
-    if (e == cudaSuccess) e = launch_seq_tc(p, D, KIND == SEQ_KV8, st);
-  } else if (e == cudaSuccess) {
-    static DeviceOnce once;
-    e = allow_smem(seq_simt_kernel<T, D, KIND>, SimtPlan<D>::kSmem, once);
-    if (e == cudaSuccess)
-      e = launch_after(seq_simt_kernel<T, D, KIND>, dim3(p.ctas), dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
-    ++launches;
   }
   if constexpr (KIND == SEQ_PLAIN) {
     if (e == cudaSuccess && p.N > 0) {
