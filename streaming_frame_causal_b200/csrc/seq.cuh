@@ -52,7 +52,7 @@ struct SeqParams {
   uint64_t* score;        // [B * Hkv, blocks] sortable
   const void* k_prefix;   // [N, Hkv, D]
   const void* v_prefix;
-  int4* share;            // [teams] {sequence, first tile of it, tiles}
+  int4* share;            // [teams] {sequence, first tile of it, tiles, the sequence's tokens}
   int2* own;              // [B] {first team that holds tiles of the sequence, teams that do}
   int* count;             // [B * items] pieces of an item that are done
   float* part_o;          // [slots, part_rows, D]
@@ -73,20 +73,22 @@ struct SeqParams {
   float scale_log2;
 };
 
+// Loads here come one after another on the way to a CTA's first tile, so what
+// follows from pos[b] is formed from one load of it.
+
 // tokens of sequence b in the cache, the new one included (0: an idle row)
 SWA_DEV int seq_tokens(const SeqParams& p, int b) {
   const long long pos = p.pos[b];
   return pos < 0 ? 0 : (pos >= p.W - 1 ? p.W : static_cast<int>(pos) + 1);
 }
 
-// places and tiles of each item of sequence b
-SWA_DEV int seq_places(const SeqParams& p, int b) {
-  const int n = seq_tokens(p, b);
+// places and tiles of each item of a sequence of n tokens
+SWA_DEV int seq_places(const SeqParams& p, int n) {
   if (p.block == 0) return (n + kSeqPlace - 1) / kSeqPlace;
   const int blocks = min((n + p.block - 1) / p.block, p.n_select);
   return (blocks * p.block + kSeqPlace - 1) / kSeqPlace;
 }
-SWA_DEV int seq_tiles(const SeqParams& p, int b) { return (seq_places(p, b) + kSeqTile - 1) / kSeqTile; }
+SWA_DEV int seq_tiles(const SeqParams& p, int n) { return (seq_places(p, n) + kSeqTile - 1) / kSeqTile; }
 
 // team that owns place t of the line of T >= teams: the c with c T / C <= t < (c + 1) T / C
 SWA_DEV int seq_owner(int64_t t, int64_t T, int teams) { return static_cast<int>(((t + 1) * teams - 1) / T); }
@@ -99,7 +101,7 @@ struct SeqRun {
 
 // Walks a CTA's share.  Every role of a CTA walks it for itself.
 struct SeqWalk {
-  int cta, item, b, t0, left, of;
+  int cta, item, b, t0, left, of, tokens;
   SWA_DEV void start(const SeqParams& p, int c) {
     cta = c;
     item = c % p.items;
@@ -107,19 +109,21 @@ struct SeqWalk {
     b = s.x;
     t0 = s.y;
     left = s.z;
-    of = left > 0 ? seq_tiles(p, b) : 0;
+    tokens = s.w;
+    of = seq_tiles(p, tokens);
   }
   SWA_DEV bool next(const SeqParams& p, SeqRun& r) {
     if (left <= 0) return false;
     while (t0 >= of) {  // on to the next sequence that has keys
       if (++b >= p.B) return false;
       t0 = 0;
-      of = seq_tiles(p, b);
+      tokens = seq_tokens(p, b);
+      of = seq_tiles(p, tokens);
     }
     r.b = b;
     r.t0 = t0;
     r.tiles = min(left, of - t0);
-    r.tokens = seq_tokens(p, b);
+    r.tokens = tokens;
     // with a shared prefix every item is merged with the prefix's pieces
     r.slot = r.tiles == of ? (p.N > 0 ? 2 * p.ctas + b * p.items + item : -1) : 2 * cta + (t0 == 0 ? 1 : 0);
     left -= r.tiles;
@@ -128,17 +132,56 @@ struct SeqWalk {
   }
 };
 
-// The pieces o(i) = [D] sums, ml(i) = {maximum, sum} for i < n, merged by a warp: lane
-// ``lane`` returns its D / 32 elements of sum_i 2^(m_i - M) O_i, and L = sum_i 2^(m_i - M) l_i.
-// A lane holds one piece's weight, and the outputs are added with independent loads
-// (from L2: other SMs have just written them).
-template <int D, int Unroll, typename O, typename ML>
+// D / 32 consecutive floats from L2 (where other SMs may just have written them)
+template <int E>
+SWA_DEV void load_l2(const float* x, float* v) {
+  if constexpr (E == 4) {
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(x));
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else if constexpr (E == 2) {
+    const float2 u = __ldcg(reinterpret_cast<const float2*>(x));
+    v[0] = u.x; v[1] = u.y;
+  } else {
+    v[0] = __ldcg(x);
+  }
+}
+
+// The pieces o(i) = [D] sums, ml(i) = {maximum, sum} for i = first, first + stride, ... < n,
+// merged by a warp: lane ``lane`` returns its D / 32 elements of sum_i 2^(m_i - M) O_i, and
+// M and L = sum_i 2^(m_i - M) l_i.  What a merge takes is the latency of its loads.  A lane
+// holds one piece's weight, and the outputs are added Unroll at a time; where few pieces
+// are usual (Few), up to 8 are loaded at once instead, weights and outputs together
+// (38.6 -> 37.0 us for 33 sequences cut 55 times).
+template <int D, int Unroll, bool Few, typename O, typename ML>
 SWA_DEV void merge_pieces(int n, int stride, int first, int lane, O o_of, ML ml_of, float* acc, float& M, float& L) {
   constexpr int E = D / 32;
   M = -INFINITY;
   L = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  if (Few && n <= first + 8 * stride) {
+    float2 ml[8];
+    float v[8][E];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (first + k * stride < n) {
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(ml_of(first + k * stride)));
+        load_l2<E>(o_of(first + k * stride) + lane * E, v[k]);
+      }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (first + k * stride < n) M = fmaxf(M, ml[k].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (first + k * stride < n) {
+        const float w = exp2f(ml[k].x - ref);
+        L += w * ml[k].y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+      }
+    return;
+  }
   for (int i0 = first; i0 < n; i0 += 32 * stride) {
     const int i = i0 + lane * stride;
     float2 ml = make_float2(-INFINITY, 0.f);
@@ -160,17 +203,8 @@ SWA_DEV void merge_pieces(int n, int stride, int first, int lane, O o_of, ML ml_
 #pragma unroll Unroll
     for (int k = 0; k < k1; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float* o = o_of(i0 + k * stride) + lane * E;
       float v[E];
-      if constexpr (E == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(o));
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else if constexpr (E == 2) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(o));
-        v[0] = x.x; v[1] = x.y;
-      } else {
-        v[0] = __ldcg(o);
-      }
+      load_l2<E>(o_of(i0 + k * stride) + lane * E, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, v[e], acc[e]);
     }

@@ -59,7 +59,7 @@ SWA_DEV void seq_divide(const SeqParams& p) {
   int T = 0, tiles = 0, n;
   for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
     const int b = b0 + threadIdx.x;
-    const int mine = b < p.B ? seq_places(p, b) : 0;
+    const int mine = b < p.B ? seq_places(p, seq_tokens(p, b)) : 0;
     int2 before;
     before.x = T + block_sum(mine > 0 ? mine + kSeqStart : 0, n);
     T += n;
@@ -90,13 +90,14 @@ SWA_DEV void seq_divide(const SeqParams& p) {
       const int first = find(t, s.x);
       s.y = first - p.own[s.x].y;
       s.z = (end < T ? find(end, other) : tiles) - first;
+      s.w = seq_tokens(p, s.x);
     }
     p.share[c] = s;
   }
   __syncthreads();
   for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
     // tile j is the last team's that begins at place 4 j + 3 of the sequence or before it
-    const int of = seq_places(p, b), t = p.own[b].x + kSeqStart;
+    const int of = seq_places(p, seq_tokens(p, b)), t = p.own[b].x + kSeqStart;
     int2 s = make_int2(0, 0);
     if (of > 0) {
       s.x = seq_owner(t + min(kSeqTile, of) - 1, T, teams);
@@ -889,7 +890,7 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
     for (int h = threadIdx.x >> 5; h < rows; h += kSimtThreads / 32) {
       const SeqPieces at{p, b, walk.item, h, own};
       float acc[D / 32], M, L;
-      merge_pieces<D, 4>(
+      merge_pieces<D, 4, true>(
           own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },
           [&](int k) { return p.part_ml + at.at(k) * 2; }, acc, M, L);
       T* out = static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.Hq + kvh * p.G + g0 + h) * D + lane * (D / 32);
@@ -959,7 +960,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const __grid_constant
   const SeqPieces at{p, b, kvh * p.groups + g / kSeqRows, g % kSeqRows, own};
   auto prefix = [&](int i) { return static_cast<int64_t>(i - pieces) * p.B * p.Hq + u; };
   float acc[E], M, L;
-  merge_pieces<D, 8>(
+  merge_pieces<D, 8, false>(
       pieces ? pieces + p.splits : 0, p.merge_warps, wi, lane,
       [&](int i) { return i < pieces ? p.part_o + at.at(i) * D : p.pre_o + prefix(i) * D; },
       [&](int i) { return i < pieces ? p.part_ml + at.at(i) * 2 : p.pre_ml + prefix(i) * 2; }, acc, M, L);

@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, ERR_WAIT_SOFTMAX));
     };
-    int cut[2], n_cut = 0;  // sequences whose item this CTA holds a part of
+    int cut[2] = {0, 0}, n_cut = 0;  // sequences whose item this CTA holds a part of,
+    int2 own[2];                      // and the teams that do
     // This key's place and exponents, and the queries' scales, are loaded a tile (a
     // sequence) ahead of their use.
     SeqRun ahead;
@@ -615,7 +616,11 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
         }
       }
       tc_fence_before();
-      if (run.slot >= 0 && p.N == 0) cut[n_cut++ & 1] = b;
+      if (run.slot >= 0 && p.N == 0) {
+        cut[n_cut] = b;
+        own[n_cut] = p.own[b];
+        ++n_cut;
+      }
       // the sums are rewritten only after the next item's first exchange, which every
       // thread reaches after reading them here
     }
@@ -627,19 +632,18 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       if (exchange()) {
         if (r < n_cut) {
           const int b = r == 0 ? cut[0] : cut[1];
-          flag[r] = atomicAdd(p.count + b * p.items + kvh, 1) == p.own[b].y - 1;
+          flag[r] = atomicAdd(p.count + b * p.items + kvh, 1) == (r == 0 ? own[0].y : own[1].y) - 1;
         }
         if (exchange()) {
           __threadfence();
           for (int i = 0; i < n_cut; ++i) {
             if (!flag[i]) continue;
             const int b = i == 0 ? cut[0] : cut[1];
-            const int2 own = p.own[b];
             for (int h = quarter; h < p.G; h += 4) {
-              const SeqPieces at{p, b, kvh, h, own};
+              const SeqPieces at{p, b, kvh, h, i == 0 ? own[0] : own[1]};
               float acc[D / 32], M, L;
-              merge_pieces<D, 4>(
-                  own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },
+              merge_pieces<D, 4, true>(
+                  at.own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },
                   [&](int k) { return p.part_ml + at.at(k) * 2; }, acc, M, L);
               uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) +
                                                           (static_cast<int64_t>(b) * p.Hq + kvh * p.G + h) * D) +

@@ -324,3 +324,265 @@ def test_many_units_for_a_cta(swa, op, G, D, dtype):
     check_decode(out, np64(ref).reshape(B, Hq, D), np64(scale).reshape(B, Hq, D), dtype,
                  np64(q) if op == "kv8" else None, np64(k) if op == "kv8" else None, op)
     assert (out[4] == 0).all()
+
+
+# ------------------------------------------------------------------ hard values
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_kv8_scales_of_all_sizes_and_far_scores(swa, dtype):
+    """Keys and values whose rows span the range of the scales, scores that climb from tile to
+    tile, one row of values far above the others, and zero rows."""
+    B, W, Hq, Hkv, D = 2, 900, 8, 2, 64
+    q, kn, vn = randn((B, Hq, D), 1, dtype, 3.0), randn((B, Hkv, D), 2, dtype), randn((B, Hkv, D), 3, dtype)
+    k, v = randn((B, W, Hkv, D), 4, dtype), randn((B, W, Hkv, D), 5, dtype)
+    k *= torch.linspace(0.05, 3.0, W, device="cuda").view(1, W, 1, 1).to(dtype)
+    e = torch.randint(-12, 12, (B, W, Hkv, 1), generator=torch.Generator().manual_seed(6)).float().cuda()
+    v = (v.float() * torch.exp2(e)).to(dtype)
+    k[0, 100:140], v[0, 300:340], q[1, 3] = 0.0, 0.0, 0.0
+    v[1, 17] *= 2.0 ** 20
+    pos = torch.tensor([W + 3, W - 200])
+    cache = new_cache8(B, W, Hkv, D)
+    swa.swa_kv8_write(k, v, *cache, torch.zeros(B, dtype=torch.int64).cuda(), count=torch.tensor([W, W - 200]).int().cuda())
+    kc, vc = values8(*cache[:2]), values8(*cache[2:])
+    new = [a * 2.0 ** x[..., None] for a, x in (orc.quantise8(np64(kn)), orc.quantise8(np64(vn)))]
+    ref, scale, kc, vc = orc.decode_step(np64(q), *new, kc, vc, pos.numpy())
+    out = torch.empty_like(q)
+    swa.swa_decode_kv8(q, kn, vn, *cache, pos.cuda(), out)
+    check_decode(out, ref, scale, dtype, np64(q), np.where(np.isnan(kc), 0.0, kc), "kv8 scales")
+
+
+def test_nan_stays_in_its_own_rows(swa):
+    """A NaN query head, or NaN in one sequence's valid keys, reaches no other output."""
+    B, W, Hq, Hkv, D = 3, 400, 8, 2, 128
+    pos = torch.tensor([399, 250, 30]).cuda()
+    for op in ("kv8", "prefix", "sparse"):
+        q, kn, vn = (randn((B, h, D), s, BF16) for h, s in ((Hq, 1), (Hkv, 2), (Hkv, 3)))
+        k, v = randn((B, W, Hkv, D), 4, BF16), randn((B, W, Hkv, D), 5, BF16)
+        outs = []
+        for bad in (False, True):
+            qq, kk, vv = q.clone(), k.clone(), v.clone()
+            if bad:
+                qq[0, 2] = float("nan")
+                vv[1, 7, 1] = float("nan")
+                kk[2, 3, 0] = float("nan")
+            out = torch.empty_like(q)
+            if op == "kv8":
+                cache = new_cache8(B, W, Hkv, D)
+                swa.swa_kv8_write(kk, vv, *cache, torch.zeros_like(pos))
+                swa.swa_decode_kv8(qq, kn, vn, *cache, pos, out)
+            elif op == "prefix":
+                swa.swa_decode_prefix(qq, kn, vn, k[0, :300].contiguous(), v[0, :300].contiguous(), kk, vv, pos, out)
+            else:
+                bounds = torch.empty(B, Hkv, 25, 2, D, dtype=BF16, device="cuda")
+                swa.swa_block_bounds(kk, pos, bounds, 16)
+                sel = torch.empty(B, Hkv, 25, dtype=torch.int32, device="cuda")
+                swa.swa_decode_sparse(qq, kn, vn, kk, vv, bounds, pos, out, sel, 16)
+            outs.append(out)
+        hit = torch.zeros(B, Hq, dtype=torch.bool, device="cuda")
+        hit[0, 2] = hit[1, 4:] = hit[2, :4] = True
+        assert torch.isnan(outs[1]).all(2).equal(hit), op
+        assert torch.equal(outs[0][~hit], outs[1][~hit]), op
+    assert swa.swa_device_error_check() == 0
+
+
+def test_sparse_selection_of_equal_and_close_scores(swa):
+    """Many blocks whose scores are equal, or differ by less than 32-bit sums can tell."""
+    B, W, Hkv, D, block, n_select = 1, 4000, 2, 128, 16, 37
+    for dtype, step in ((BF16, 2.0 ** -7), (F32, 2.0 ** -23)):
+        g = torch.Generator().manual_seed(3)
+        row = torch.randn(1, 1, Hkv, D, generator=g).to(dtype)
+        k = row.repeat(B, W, 1, 1).cuda()
+        # in every fifth block one element of one key is a step off
+        j = torch.arange(0, W // block, 5)
+        k[0, j * block + 3, :, 5] = k[0, j * block + 3, :, 5] * (1 + step * (1 + j % 3)).view(-1, 1).to(dtype).cuda()
+        v = randn((B, W, Hkv, D), 5, dtype)
+        q, kn, vn = randn((B, 8, D), 6, dtype), k[:, 0].clone(), randn((B, Hkv, D), 7, dtype)
+        pos = torch.tensor([W - 1])
+        bounds = torch.empty(B, Hkv, W // block, 2, D, dtype=dtype, device="cuda")
+        swa.swa_block_bounds(k, pos.cuda(), bounds, block)
+        sel = torch.empty(B, Hkv, n_select, dtype=torch.int32, device="cuda")
+        out = torch.empty_like(q)
+        swa.swa_decode_sparse(q, kn, vn, k, v, bounds, pos.cuda(), out, sel, block, n_first=1, n_last=2)
+        want = orc.select_blocks(np64(q), np64(bounds), pos.numpy(), W, block, n_select, 1, 2)
+        np.testing.assert_array_equal(sel.cpu().numpy()[0], np.array(want[0]))
+
+
+def test_sparse_more_blocks_than_shared_memory_keeps(swa):
+    """A row of 2500 blocks, infinite and NaN keys among them: the first two go by their bounds, a NaN score comes last."""
+    B, W, Hkv, D, block, n_select = 2, 40000, 1, 64, 16, 300
+    q, kn, vn = (randn((B, h, D), s, BF16) for h, s in ((4, 1), (Hkv, 2), (Hkv, 3)))
+    k, v = randn((B, W, Hkv, D), 4, BF16), randn((B, W, Hkv, D), 5, BF16)
+    pos = torch.tensor([W - 5, 3 * W + 11])
+    k[0, 777, 0, 3] = float("nan")       # passed over
+    bounds = torch.empty(B, Hkv, W // block, 2, D, dtype=BF16, device="cuda")
+    swa.swa_block_bounds(k, pos.cuda() - 1, bounds, block)
+    bounds[0, 0, 100, 0, 1] = float("nan")  # a block whose score is NaN
+    bounds[1, 0, 200, 1, 2] = 3e38          # a score that 32 bits may not hold
+    bounds[1, 0, 201, 0, 2] = -3e38
+    sel = torch.empty(B, Hkv, n_select, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    swa.swa_decode_sparse(q, kn, vn, k, v, bounds, pos.cuda(), out, sel, block)
+    b64 = np64(bounds)
+    b64[0, 0, 100] = -1e300 * np.sign(np64(q[0]).sum(0))  # behind every number
+    with np.errstate(invalid="ignore"):
+        want = orc.select_blocks(np64(q), b64, pos.numpy(), W, block, n_select, 1, 1)
+    assert 100 not in sel[0].tolist()
+    np.testing.assert_array_equal(sel.cpu().numpy()[1, 0], np.array(want[1][0]))
+    got0, want0 = set(sel[0, 0].tolist()), set(want[0][0])
+    assert got0 == want0
+    assert swa.swa_device_error_check() == 0
+
+
+# ------------------------------------------------------------------ as they are used
+def test_steps_captured_once_and_replayed(swa):
+    """One captured step of each kind, replayed while positions, queries and new tokens change in place:
+    every replay equals the call made anew on the same values."""
+    B, W, Hq, Hkv, D, N, block = 3, 150, 8, 2, 64, 200, 16
+    pos = torch.tensor([0, 140, 148]).cuda()
+    q, kn, vn = (torch.empty(B, h, D, dtype=BF16, device="cuda") for h in (Hq, Hkv, Hkv))
+    k, v = randn((B, W, Hkv, D), 4, BF16), randn((B, W, Hkv, D), 5, BF16)
+    kp, vp = randn((N, Hkv, D), 6, BF16), randn((N, Hkv, D), 7, BF16)
+    sel = torch.empty(B, Hkv, 5, dtype=torch.int32, device="cuda")
+
+    def state():
+        c8 = new_cache8(B, W, Hkv, D)
+        swa.swa_kv8_write(k, v, *c8, torch.zeros_like(pos))
+        bounds = torch.empty(B, Hkv, -(-W // block), 2, D, dtype=BF16, device="cuda")
+        swa.swa_block_bounds(k, pos - 1, bounds, block)
+        return c8, [k.clone(), v.clone()], [k.clone(), v.clone()], bounds, [torch.empty_like(q) for _ in range(3)]
+
+    def step(s):
+        c8, c1, c2, bounds, out = s
+        swa.swa_decode_kv8(q, kn, vn, *c8, pos, out[0])
+        swa.swa_decode_prefix(q, kn, vn, kp, vp, *c1, pos, out[1])
+        swa.swa_decode_sparse(q, kn, vn, *c2, bounds, pos, out[2], sel, block)
+
+    def draw(i):
+        for t, s in ((q, 1), (kn, 2), (vn, 3)):
+            t.copy_(randn(tuple(t.shape), 10 * i + s, BF16))
+
+    draw(0)
+    warm = state()
+    step(warm)
+    a, b = state(), state()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a)
+    for i in range(6):
+        draw(i)
+        graph.replay()
+        step(b)
+        for x, y in zip(a[4], b[4]):
+            assert torch.equal(x, y) and torch.isfinite(x).all()
+        pos += 1
+    for x, y in zip(a[0] + a[1] + a[2] + [a[3]], b[0] + b[1] + b[2] + [b[3]]):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert swa.swa_device_error_check() == 0
+
+
+def test_repeated_steps_give_the_same_bits(swa):
+    B, W, Hq, Hkv, D = 9, 1500, 16, 4, 128
+    pos = lengths(B, W, 3).cuda()
+    q, kn, vn = (randn((B, h, D), s, BF16) for h, s in ((Hq, 1), (Hkv, 2), (Hkv, 3)))
+    k, v = randn((B, W, Hkv, D), 4, BF16), randn((B, W, Hkv, D), 5, BF16)
+    kp, vp = randn((700, Hkv, D), 6, BF16), randn((700, Hkv, D), 7, BF16)
+    c8 = new_cache8(B, W, Hkv, D)
+    swa.swa_kv8_write(k, v, *c8, torch.zeros_like(pos))
+    first = None
+    for _ in range(20):
+        out = [torch.empty_like(q) for _ in range(2)]
+        swa.swa_decode_kv8(q, kn, vn, *c8, pos, out[0])
+        swa.swa_decode_prefix(q, kn, vn, kp, vp, k, v, pos, out[1])
+        first = first or out
+        assert all(torch.equal(x, y) for x, y in zip(first, out))
+
+
+def test_another_stream_and_a_workspace_of_the_callers(swa):
+    B, W, Hq, Hkv, D = 4, 600, 8, 2, 64
+    pos = lengths(B, W, 5).cuda()
+    q, kn, vn = (randn((B, h, D), s, BF16) for h, s in ((Hq, 1), (Hkv, 2), (Hkv, 3)))
+    k, v = randn((B, W, Hkv, D), 4, BF16), randn((B, W, Hkv, D), 5, BF16)
+    ref = torch.empty_like(q)
+    swa.swa_decode_prefix(q, kn, vn, k[0], v[0], k, v, pos, ref)
+    nbytes = swa.swa_decode_prefix_workspace_bytes(B, Hq, Hkv, D, W, W)
+    ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")  # what it holds before does not matter
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [torch.empty_like(q) for _ in range(3)]
+    swa.swa_decode_prefix(q, kn, vn, k[0], v[0], k, v, pos, outs[0], stream=side)
+    swa.swa_decode_prefix(q, kn, vn, k[0], v[0], k, v, pos, outs[1], workspace=ws, stream=side.cuda_stream)
+    with torch.cuda.stream(side):
+        swa.swa_decode_prefix(q, kn, vn, k[0], v[0], k, v, pos, outs[2], workspace=ws)
+    side.synchronize()
+    assert all(torch.equal(ref, o) for o in outs)
+    with pytest.raises(swa.SwaError) as e:
+        swa.swa_decode_prefix(q, kn, vn, k[0], v[0], k, v, pos, ref, workspace=ws[:nbytes - 256])
+    assert e.value.status == -4
+
+
+def test_offsets_past_32_bits(swa):
+    """The second sequence's rows begin past 2^31 elements (8-bit rows: bytes) of the cache."""
+    B, W, Hkv, G, D = 2, 1_100_000, 8, 2, 128
+    Hq = Hkv * G
+    g = torch.Generator(device="cuda").manual_seed(1)
+    c8 = [torch.randint(0, 0x7E, (B, W, Hkv, D), generator=g, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+          if i % 2 == 0 else torch.randint(116, 121, (B, Hkv, W), generator=g, dtype=torch.uint8, device="cuda") for i in range(4)]
+    q, kn, vn = (torch.randn(B, h, D, generator=g, device="cuda").to(BF16) * 0.02 for h in (Hq, Hkv, Hkv))
+    pos = torch.tensor([5, W - 300_000]).cuda()
+    out = torch.empty_like(q)
+    swa.swa_decode_kv8(q, kn, vn, *c8, pos, out)
+    back = [torch.empty(B, 3, Hkv, D, dtype=F32, device="cuda") for _ in range(2)]
+    swa.swa_kv8_read(*c8, pos - 2, *back)
+    n = int(pos[1]) + 1
+    for h in (0, 3, 7):
+        k, v = (c8[i][1, :n, h].double() * torch.exp2(c8[i + 1][1, h, :n].double() - 127)[:, None] for i in (0, 2))
+        assert torch.equal(back[0][1, :, h].double(), k[-3:]) and torch.equal(back[1][1, :, h].double(), v[-3:])
+        s = q[1, h * G:(h + 1) * G].double() @ k.t() / D ** 0.5
+        p = torch.softmax(s, -1)
+        check_decode(out[1, h * G:(h + 1) * G], np64(p @ v), np64(p @ v.abs()), BF16,
+                     np64(q[1]), np64(k.abs().sum(-1).max().view(1, 1)), "far offsets")
+    assert swa.swa_device_error_check() == 0
+
+
+def test_a_run_of_the_operators_together(swa):
+    """Rotated keys enter a 16-bit and an 8-bit cache; then steps with a shared prefix, over selected blocks (all of
+    them fit) and over the 8-bit cache, against float64 on the same values."""
+    B, T, W, Hq, Hkv, D, N, block = 2, 90, 96, 8, 2, 64, 50, 32
+    pairs = (12, 10, 10)
+    grid = lambda t: torch.stack([t // 9, t // 3 % 3, t % 3], -1).to(torch.int32).cuda()  # noqa: E731
+    rows = randn((B, T, Hkv + Hkv, D), 1, BF16)  # k beside v
+    k, v = rows[:, :, :Hkv], rows[:, :, Hkv:].contiguous()
+    k = swa.swa_rope_nd(k, grid(torch.arange(T)).expand(B, T, 3).contiguous(), pairs)
+    kp, vp = randn((N, Hkv, D), 2, BF16), randn((N, Hkv, D), 3, BF16)
+    swa.swa_rope_nd(kp, grid(torch.arange(N)), pairs, out=kp)
+    kc, vc = (torch.zeros(B, W, Hkv, D, dtype=BF16, device="cuda") for _ in range(2))
+    kc[:, :T], vc[:, :T] = k, v
+    ks, vs = kc.clone(), vc.clone()
+    c8 = new_cache8(B, W, Hkv, D)
+    start = torch.zeros(B, dtype=torch.int64, device="cuda")
+    swa.swa_kv8_write(k, v, *c8, start)
+    pos = start + T - 1
+    bounds = torch.zeros(B, Hkv, W // block, 2, D, dtype=BF16, device="cuda")
+    swa.swa_block_bounds(ks, pos, bounds, block)
+    sel = torch.empty(B, Hkv, W // block, dtype=torch.int32, device="cuda")
+    k64, v64 = np64(kc), np64(vc)
+    k8, v8 = values8(*c8[:2]), values8(*c8[2:])
+    for i in range(10):  # past the end of the window
+        pos += 1
+        at = grid(pos.cpu()).view(B, 3)
+        q = swa.swa_rope_nd(randn((B, Hq, D), 20 + i, BF16), at, pairs)
+        kn = swa.swa_rope_nd(randn((B, Hkv, D), 40 + i, BF16), at, pairs)
+        vn = randn((B, Hkv, D), 60 + i, BF16)
+        outs = [torch.empty_like(q) for _ in range(3)]
+        swa.swa_decode_prefix(q, kn, vn, kp, vp, kc, vc, pos, outs[0])
+        swa.swa_decode_sparse(q, kn, vn, ks, vs, bounds, pos, outs[1], sel, block)
+        swa.swa_decode_kv8(q, kn, vn, *c8, pos, outs[2])
+        p = pos.cpu().numpy()
+        ref, scale, k2, v2 = orc.decode_step(np64(q), np64(kn), np64(vn), k64, v64, p, prefix=(np64(kp), np64(vp)))
+        check_decode(outs[0], ref, scale, BF16, what="prefix")
+        ref, scale, k64, v64 = orc.decode_step(np64(q), np64(kn), np64(vn), k64, v64, p)
+        check_decode(outs[1], ref, scale, BF16, what="all blocks")
+        new = [a * 2.0 ** e[..., None] for a, e in (orc.quantise8(np64(kn)), orc.quantise8(np64(vn)))]
+        ref, scale, k8, v8 = orc.decode_step(np64(q), *new, k8, v8, p)
+        check_decode(outs[2], ref, scale, BF16, np64(q), np.where(np.isnan(k8), 0.0, k8), "8 bits")
+    assert torch.equal(kc, ks) and torch.equal(vc, vs)
+    assert swa.swa_device_error_check() == 0
