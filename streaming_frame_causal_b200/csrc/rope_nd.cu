@@ -130,6 +130,34 @@ __global__ void __launch_bounds__(kRopeThreads) rope_nd_kernel(const __grid_cons
   for (int i = threadIdx.x + kRopeAhead * kRopeThreads; i < n; i += kRopeThreads) put(i, get(i));
 }
 
+// The bands' first pairs and rates.  64 powers take as long as a launch, and a program's
+// calls have one theta and one split into bands, so a thread keeps the last ones.
+void rope_rates(double theta, int axes, const int32_t* pairs, RopeParams& p) {
+  struct Rates {
+    double theta = 0.0, rate[kRopeMaxPairs];
+    int axes = 0, pairs[kRopeMaxAxes];
+  };
+  static thread_local Rates last;
+  bool same = last.theta == theta && last.axes == axes;
+  for (int a = 0; a < axes && same; ++a) same = last.pairs[a] == pairs[a];
+  if (!same) {
+    last.theta = theta;
+    last.axes = axes;
+    int n = 0;
+    for (int a = 0; a < axes; ++a) {
+      last.pairs[a] = pairs[a];
+      for (int j = 0; j < pairs[a]; ++j)
+        last.rate[n++] = std::pow(theta, -static_cast<double>(j) / pairs[a]) * 0.15915494309189533576889;
+    }
+  }
+  int n = 0;
+  for (int a = 0; a < axes; ++a) {
+    p.first[a] = n;
+    n += pairs[a];
+  }
+  std::copy(last.rate, last.rate + n, p.rate);
+}
+
 }  // namespace
 }  // namespace swa
 
@@ -147,12 +175,10 @@ extern "C" swa_status swa_rope_nd(const void* x, void* y, const int32_t* pos, lo
   if (row > (1 << 20) || x_row_stride < row || y_row_stride < row) return SWA_ERR_SHAPE;
   if (x_row_stride > (1ll << 40) || y_row_stride > (1ll << 40) || tokens > (1ll << 40)) return SWA_ERR_SHAPE;
   if (x_row_stride * esize % 16 || y_row_stride * esize % 16) return SWA_ERR_ARG;
-  RopeParams p{};
   int n = 0;
   for (int a = 0; a < axes; ++a) {
     if (pairs[a] < 0 || pairs[a] > head_dim / 2 - n) return SWA_ERR_SHAPE;
-    p.first[a] = n;
-    for (int j = 0; j < pairs[a]; ++j) p.rate[n++] = std::pow(theta, -static_cast<double>(j) / pairs[a]) * 0.15915494309189533576889;
+    n += pairs[a];
   }
   if (tokens == 0) return SWA_OK;
   if (!x || !y || !pos) return SWA_ERR_ARG;
@@ -160,6 +186,8 @@ extern "C" swa_status swa_rope_nd(const void* x, void* y, const int32_t* pos, lo
   if (reinterpret_cast<uintptr_t>(pos) & 3u) return SWA_ERR_ARG;
   int* err = nullptr;
   if (const int ds = device_ready_status(&err)) return static_cast<swa_status>(ds);
+  RopeParams p{};
+  rope_rates(theta, axes, pairs, p);
   p.x = static_cast<const uint8_t*>(x);
   p.y = static_cast<uint8_t*>(y);
   p.pos = pos;

@@ -76,11 +76,12 @@ struct SeqParams {
 // Loads here come one after another on the way to a CTA's first tile, so what
 // follows from pos[b] is formed from one load of it.
 
-// tokens of sequence b in the cache, the new one included (0: an idle row)
-SWA_DEV int seq_tokens(const SeqParams& p, int b) {
-  const long long pos = p.pos[b];
+// tokens in the cache of a sequence at pos, the new one included (0: an idle row)
+SWA_DEV int seq_tokens_at(const SeqParams& p, long long pos) {
   return pos < 0 ? 0 : (pos >= p.W - 1 ? p.W : static_cast<int>(pos) + 1);
 }
+
+SWA_DEV int seq_tokens(const SeqParams& p, int b) { return seq_tokens_at(p, p.pos[b]); }
 
 // places and tiles of each item of a sequence of n tokens
 SWA_DEV int seq_places(const SeqParams& p, int n) {
@@ -99,9 +100,12 @@ struct SeqRun {
   int slot;                  // partial slot; -1: the item is whole, its output is written
 };
 
-// Walks a CTA's share.  Every role of a CTA walks it for itself.
+// Walks a CTA's share.  Every role of a CTA walks it for itself, and has the position of
+// the sequence behind the present one loaded before it gets there (a load at every change
+// of sequence, in each role after the other, took 3 us of it).
 struct SeqWalk {
   int cta, item, b, t0, left, of, tokens;
+  long long pos1;
   SWA_DEV void start(const SeqParams& p, int c) {
     cta = c;
     item = c % p.items;
@@ -111,14 +115,16 @@ struct SeqWalk {
     left = s.z;
     tokens = s.w;
     of = seq_tiles(p, tokens);
+    pos1 = p.pos[min(b + 1, p.B - 1)];
   }
   SWA_DEV bool next(const SeqParams& p, SeqRun& r) {
     if (left <= 0) return false;
     while (t0 >= of) {  // on to the next sequence that has keys
       if (++b >= p.B) return false;
       t0 = 0;
-      tokens = seq_tokens(p, b);
+      tokens = seq_tokens_at(p, pos1);
       of = seq_tiles(p, tokens);
+      pos1 = p.pos[min(b + 1, p.B - 1)];
     }
     r.b = b;
     r.t0 = t0;

@@ -448,23 +448,27 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
         uint32_t sv[16];
         tmem_ld16(tmem + lane_off + sb * kN, sv);
         tmem_wait_ld();
-        if (!valid) {
-          // The key's V row in the tile is whatever the slot or the unit held.  Its weight
-          // is 0, but 0 x NaN is NaN, so the row is zeroed, once V has landed, before the
-          // second product reads it (the proxy fence before the p_full arrival orders
-          // these stores first).
+        const unsigned bad = __ballot_sync(0xffffffffu, !valid);
+        if (bad) {
+          // The V row of a key behind the valid ones is whatever the slot or the unit held.
+          // Its weight is 0, but 0 x NaN is NaN, so the row is zeroed, once V has landed,
+          // before the second product reads it (the proxy fence before the p_full arrival
+          // orders these stores first).  The warp's lanes write whole rows side by side: a
+          // lane to each of its own rows would find 32 lanes in the same banks.
           const int u = v_unit(jj);
-          if (!mbar_wait(kv_full(u % kUnits), (u / kUnits) & 1, p.err, ERR_WAIT_SOFTMAX)) ok = false;
-          const uint32_t vrow = base + (u % kUnits) * PL::kUnit + r * PL::kSubBytesRow;
+          ok = wait(kv_full(u % kUnits), (u / kUnits) & 1);
+          constexpr int kLanesRow = PL::kSubBytesRow / 16;
+          const uint32_t rows0 = base + (u % kUnits) * PL::kUnit + quarter * 32 * PL::kSubBytesRow;
 #pragma unroll
-          for (int sub = 0; sub < PL::kSubs; ++sub)
+          for (int i = 0; i < kLanesRow; ++i) {
+            const int row = i * (32 / kLanesRow) + lane / kLanesRow;
+            if (bad >> row & 1)
 #pragma unroll
-            for (int o = 0; o < PL::kSubBytesRow; o += 16) st_zero16(vrow + sub * PL::kSub + o);
+              for (int sub = 0; sub < PL::kSubs; ++sub)
+                st_zero16(rows0 + sub * PL::kSub + row * PL::kSubBytesRow + lane % kLanesRow * 16);
+          }
         }
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        if (!ok) break;
         float x[GP];
         const float kscale = KV8 ? __uint_as_float(static_cast<uint32_t>(ke0) << 23) : 1.f;
         const float vexp = static_cast<float>(ve0 - 127);
