@@ -478,7 +478,7 @@ swa_status swa_kv8_read(const void* k8, const uint8_t* k_exp, const void* v8, co
  *   step refuses), 16-byte aligned; calls that share one must not overlap on the GPU.
  * bf16: head_dim 64 or 128 with Hq/Hkv from 1 to 8; f32: head_dim 32, 64 or 128, any
  * Hq/Hkv.  Errors: SWA_ERR_ARG, SWA_ERR_SHAPE (Hq not a multiple of Hkv, or sizes
- * past the limits: Hq 65535, B * Hq 2^26), SWA_ERR_UNSUPPORTED, SWA_ERR_CAPACITY
+ * past the limits: Hq 65535, B * Hq 2^26, W and N 2^30), SWA_ERR_UNSUPPORTED, SWA_ERR_CAPACITY
  * (workspace too small).
  *
  * swa_decode_kv8: on the 8-bit cache above; the new token is quantised as it is

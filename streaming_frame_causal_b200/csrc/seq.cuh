@@ -30,12 +30,14 @@ namespace swa {
 constexpr int kSeqKeys = 128;     // keys of a tile
 constexpr int kSeqRows = 8;       // query heads of an item
 constexpr int kSeqMaxCtas = 640;  // CTAs of a launch (or one team, if that is more)
-constexpr int kSeqPlace = 32;      // keys of a place
-constexpr int kSeqStart = 8;        // of 4, 8 and 12: 42.6, 41.5 and 40.5 us for 33 sequences of 82 to 8192 tokens,
-                                    // 82.5, 83.4 and 84.3 us for 64 of 20 to 512 behind a prefix
+constexpr int kSeqPlace = 32;     // keys of a place
 constexpr int kSeqTile = kSeqKeys / kSeqPlace;  // places of a tile
+// Of 0, 4 and 8 places: 36.8, 35.7 and 35.3 us for 33 sequences of 82 to 8192 tokens in 8
+// bits, 68.8, 68.8 and 67.4 us for 64 of 20 to 512 behind a prefix.
+constexpr int kSeqStart = 8;
 constexpr int kSeqCols = 16;      // query columns of the tensor-core products
 constexpr int kSeqMaxSplits = 64; // pieces of a shared prefix
+constexpr int kSeqMaxTokens = 1 << 30;  // of a cache, and of a prefix
 
 struct SeqParams {
   const void* q;          // [B, Hq, D]
@@ -49,7 +51,7 @@ struct SeqParams {
   void* out;              // [B, Hq, D]
   int* selected;          // block-sparse: [B, Hkv, n_select] ascending, -1 behind
   void* bounds;           // [B, Hkv, blocks, 2, D]
-  uint64_t* score;        // [B * Hkv, blocks] sortable
+  uint64_t* score;        // [B * Hkv, blocks] 32-bit score in sortable form, the bound on its error below
   const void* k_prefix;   // [N, Hkv, D]
   const void* v_prefix;
   int4* share;            // [teams] {sequence, first tile of it, tiles, the sequence's tokens}

@@ -4,8 +4,8 @@
 //
 // One step is a chain of kernels, each a programmatic dependent launch behind the
 // one before: the new token enters the cache and the work is divided (seq.cuh), and
-// block-sparse the blocks are scored and selected; the prefix's pieces; the attention over the
-// caches; with a prefix, the merge.
+// block-sparse the blocks are scored and selected; the attention over the caches;
+// and with a prefix the attention over it, and the merge with its pieces.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -1062,7 +1062,7 @@ swa_status seq_sizes(SeqParams& p, int D, int dtype) {
   if (p.Hq > 65535 ||
       static_cast<int64_t>(p.B) * p.items > 0x3fffffffll || static_cast<int64_t>(p.B) * p.Hq > (1ll << 26) ||
       static_cast<int64_t>(p.B) * (p.W / kSeqPlace + 2 + kSeqStart) > 0x7fffffffll ||
-      static_cast<int64_t>(p.W) * p.Hkv * D > (1ll << 37))
+      p.W > kSeqMaxTokens || p.N > kSeqMaxTokens || static_cast<int64_t>(std::max(p.W, p.N)) * p.Hkv * D > (1ll << 37))
     return SWA_ERR_SHAPE;
   p.splits = prefix_pieces(p, dtype == SWA_BF16);
   return SWA_OK;

@@ -93,7 +93,7 @@ constexpr float kPScale = 2048.f;  // 2^11: weights up to 2^(11 + 4) fit e5m2's 
 
 struct SeqTcParams {
   SeqParams s;
-  CUtensorMap tm_k, tm_v;  // [B, W, Hkv, D], box 128 rows (or a block's) of one head
+  CUtensorMap tm_k, tm_v;  // [B, W, Hkv, D], box 32 rows (or a block's) of one head
   CUtensorMap tm_q;        // bf16 [B * Hq, D], or the split queries [B * Hkv * 16, D]
 };
 
@@ -148,8 +148,8 @@ SWA_DEV uint64_t sdesc_rows(uint32_t addr, uint32_t lbo) {
   return d;
 }
 
-// e4m3 and e5m2 hold what the comments above say; a and b are the top bytes of v
-// and of what they leave, c the rounded rest (two values at a time)
+// The three e5m2 terms of two values, in the top bytes of the halves of t[0..2]: a and b are
+// the top bytes of the 16-bit floats and of what they leave, c the rounded rest.
 SWA_DEV void split_e5m2(float x0, float x1, uint32_t* t) {
   __half2 v = __floats2half2_rn(x0, x1);
 #pragma unroll
@@ -396,8 +396,9 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, ERR_WAIT_SOFTMAX));
     };
-    int cut[2] = {0, 0}, n_cut = 0;  // sequences whose item this CTA holds a part of,
-    int2 own[2];                      // and the teams that do
+    // sequences whose item this CTA holds a part of (at most two), and the teams that do
+    int n_cut = 0, cut0 = 0, cut1 = 0;
+    int2 own0 = make_int2(0, 0), own1 = own0;
     // This key's place and exponents, and the queries' scales, are loaded a tile (a
     // sequence) ahead of their use.
     SeqRun ahead;
@@ -538,6 +539,10 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
             tmem_wait_st();
           }
         }
+        // a head whose scores so far are all -inf keeps that maximum, and weights of 0
+        float ref[GP];
+#pragma unroll
+        for (int h = 0; h < GP; ++h) ref[h] = m[h] == -INFINITY ? 0.f : m[h];
         const uint32_t pb = base + PL::kOffP + sb * PL::kP;
         if constexpr (KV8) {
           // P^T rows (term, head) of 128 bytes, the 128-byte-swizzled K-major layout
@@ -548,16 +553,17 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
           };
 #pragma unroll
           for (int h = 0; h < GP; h += 2) {
-            const float e0 = ex2_approx(x[h] - m[h]);
-            const float e1 = h + 1 < GP ? ex2_approx(x[h + 1 < GP ? h + 1 : h] - m[h + 1 < GP ? h + 1 : h]) : 0.f;
+            constexpr int kNext = GP > 1 ? 1 : 0;  // one head: its pair is itself, and not written
+            const float e0 = ex2_approx(x[h] - ref[h]);
+            const float e1 = ex2_approx(x[h + kNext] - ref[h + kNext]);
             l[h] = fmaf(e0, sum_scale, l[h]);
-            if (h + 1 < GP) l[h + 1 < GP ? h + 1 : h] = fmaf(e1, sum_scale, l[h + 1 < GP ? h + 1 : h]);
+            if (kNext) l[h + kNext] = fmaf(e1, sum_scale, l[h + kNext]);
             uint32_t t[3];
             split_e5m2(e0 * kPScale, e1 * kPScale, t);
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
               put(i * GP + h, t[i] >> 8);
-              if (h + 1 < GP) put(i * GP + h + 1, t[i] >> 24);
+              if (kNext) put(i * GP + h + 1, t[i] >> 24);
             }
           }
         } else {
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
           const int col = r & 63;
 #pragma unroll
           for (int h = 0; h < GP; ++h) {
-            const float pe = ex2_approx(x[h] - m[h]);
+            const float pe = ex2_approx(x[h] - ref[h]);
             l[h] += pe;
             const __nv_bfloat16 bv = __float2bfloat16_rn(pe);
             st_b16(ph + h * 128 + ((((col >> 3) ^ (h & 7))) << 4) + (col & 7) * 2,
@@ -621,9 +627,13 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       }
       tc_fence_before();
       if (run.slot >= 0 && p.N == 0) {
-        cut[n_cut] = b;
-        own[n_cut] = p.own[b];
-        ++n_cut;
+        if (n_cut++ == 0) {
+          cut0 = b;
+          own0 = p.own[b];
+        } else {
+          cut1 = b;
+          own1 = p.own[b];
+        }
       }
       // the sums are rewritten only after the next item's first exchange, which every
       // thread reaches after reading them here
@@ -635,16 +645,16 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       __threadfence();
       if (exchange()) {
         if (r < n_cut) {
-          const int b = r == 0 ? cut[0] : cut[1];
-          flag[r] = atomicAdd(p.count + b * p.items + kvh, 1) == (r == 0 ? own[0].y : own[1].y) - 1;
+          const int b = r == 0 ? cut0 : cut1;
+          flag[r] = atomicAdd(p.count + b * p.items + kvh, 1) == (r == 0 ? own0.y : own1.y) - 1;
         }
         if (exchange()) {
           __threadfence();
           for (int i = 0; i < n_cut; ++i) {
             if (!flag[i]) continue;
-            const int b = i == 0 ? cut[0] : cut[1];
+            const int b = i == 0 ? cut0 : cut1;
             for (int h = quarter; h < p.G; h += 4) {
-              const SeqPieces at{p, b, kvh, h, i == 0 ? own[0] : own[1]};
+              const SeqPieces at{p, b, kvh, h, i == 0 ? own0 : own1};
               float acc[D / 32], M, L;
               merge_pieces<D, 4, true>(
                   at.own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },

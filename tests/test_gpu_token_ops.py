@@ -384,6 +384,31 @@ def test_nan_stays_in_its_own_rows(swa):
     assert swa.swa_device_error_check() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_keys_of_minus_infinity_have_no_weight(swa, dtype):
+    """A whole first tile of keys whose scores are -inf, then finite ones; and a row of nothing else."""
+    B, W, Hkv, D, block = 2, 300, 1, 64, 64
+    q, kn, vn = (randn((B, h, D), s, dtype) for h, s in ((3, 1), (Hkv, 2), (Hkv, 3)))
+    k, v = randn((B, W, Hkv, D), 4, dtype), randn((B, W, Hkv, D), 5, dtype)
+    q[:, :, 0] = 1.0
+    k[0, :150, :, 0] = -float("inf")
+    kn[1, :, 0] = -float("inf")
+    pos = torch.tensor([W - 1, 0]).cuda()
+    ref, scale, _, _ = orc.decode_step(np64(q[:1]), np64(kn[:1]), np64(vn[:1]), np64(k[:1]), np64(v[:1]), [W - 1])
+    for op in ("prefix", "sparse"):
+        out = torch.empty_like(q)
+        kk, vv = k.clone(), v.clone()
+        if op == "prefix":
+            swa.swa_decode_prefix(q, kn, vn, k[0, :0], v[0, :0], kk, vv, pos, out)
+        else:
+            bounds = torch.empty(B, Hkv, -(-W // block), 2, D, dtype=dtype, device="cuda")
+            swa.swa_block_bounds(kk, pos, bounds, block)
+            sel = torch.empty(B, Hkv, 5, dtype=torch.int32, device="cuda")
+            swa.swa_decode_sparse(q, kn, vn, kk, vv, bounds, pos, out, sel, block)
+        check_decode(out[:1], ref, scale, dtype, what=op)
+        assert torch.isnan(out[1]).all()  # no key has a weight: 0 / 0, as the formula says
+
+
 def test_sparse_selection_of_equal_and_close_scores(swa):
     """Many blocks whose scores are equal, or differ by less than 32-bit sums can tell."""
     B, W, Hkv, D, block, n_select = 1, 4000, 2, 128, 16, 37

@@ -93,7 +93,8 @@ def test_step_refuses_null_and_misaligned_pointers(swa, step, n):
 
 def test_prefix_and_sparse_refusals(swa):
     lib = swa._lib
-    assert prefix(lib, N=-1) == ARG
+    assert prefix(lib, N=-1) == ARG and prefix(lib, N=(1 << 30) + 1) == SHAPE
+    assert kv8(lib, W=(1 << 30) + 1) == SHAPE
     for bad, status in ((dict(block=48), UNSUPPORTED), (dict(block=0), UNSUPPORTED), (dict(sel=0), ARG),
                         (dict(first=-1), ARG), (dict(last=-1), ARG), (dict(sel=1), SHAPE), (dict(sel=1 << 21), SHAPE),
                         (dict(selected=None), ARG), (dict(selected=A + 2), ARG), (dict(B=40000), SHAPE)):
