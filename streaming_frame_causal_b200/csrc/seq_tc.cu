@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, ERR_WAIT_SOFTMAX));
     };
     // sequences whose item this CTA holds a part of (at most two), and the teams that do
-    int n_cut = 0, cut0 = 0, cut1 = 0;
-    int2 own0 = make_int2(0, 0), own1 = own0;
+    int cut[2] = {0, 0}, n_cut = 0;
+    int2 own[2];
     // This key's place and exponents, and the queries' scales, are loaded a tile (a
     // sequence) ahead of their use.
     SeqRun ahead;
@@ -627,13 +627,9 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       }
       tc_fence_before();
       if (run.slot >= 0 && p.N == 0) {
-        if (n_cut++ == 0) {
-          cut0 = b;
-          own0 = p.own[b];
-        } else {
-          cut1 = b;
-          own1 = p.own[b];
-        }
+        cut[n_cut] = b;
+        own[n_cut] = p.own[b];
+        ++n_cut;
       }
       // the sums are rewritten only after the next item's first exchange, which every
       // thread reaches after reading them here
@@ -645,16 +641,16 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
       __threadfence();
       if (exchange()) {
         if (r < n_cut) {
-          const int b = r == 0 ? cut0 : cut1;
-          flag[r] = atomicAdd(p.count + b * p.items + kvh, 1) == (r == 0 ? own0.y : own1.y) - 1;
+          const int b = r == 0 ? cut[0] : cut[1];
+          flag[r] = atomicAdd(p.count + b * p.items + kvh, 1) == (r == 0 ? own[0].y : own[1].y) - 1;
         }
         if (exchange()) {
           __threadfence();
           for (int i = 0; i < n_cut; ++i) {
             if (!flag[i]) continue;
-            const int b = i == 0 ? cut0 : cut1;
+            const int b = i == 0 ? cut[0] : cut[1];
             for (int h = quarter; h < p.G; h += 4) {
-              const SeqPieces at{p, b, kvh, h, i == 0 ? own0 : own1};
+              const SeqPieces at{p, b, kvh, h, i == 0 ? own[0] : own[1]};
               float acc[D / 32], M, L;
               merge_pieces<D, 4, true>(
                   at.own.y, 1, 0, lane, [&](int k) { return p.part_o + at.at(k) * D; },
