@@ -540,21 +540,38 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
   // the rows of a thread's blocks first, so that they are on their way
   constexpr int kIter = kScoreBlocks / kRows;
   constexpr int kAhead = kIter < 8 ? kIter : 8;
-  static_assert(kIter % kAhead == 0, "whole rounds");
+  static_assert(kIter % kAhead == 0 && 2 * kAhead <= kLanes, "whole rounds, a lane for every value");
+  constexpr int kSteps = kLanes == 32 ? 5 : kLanes == 16 ? 4 : 3;
+  constexpr int kPair = kLanes / (2 * kAhead);  // lanes apart: a block's score and its magnitudes
   const T* bounds = static_cast<const T*>(p.bounds) + row * p.n_blocks * 2 * D + part * E;
   uint4 lo[kAhead], hi[kAhead];
-  auto load = [&](int j0) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i * kRows + r;
-      if (j < used) {
-        const uint4* x = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(j) * 2 * D);
-        lo[i] = x[0];
-        hi[i] = x[D / E];
-      }
+  auto load_one = [&](int j0, int i) {
+    const int j = j0 + i * kRows + r;
+    if (j < used) {
+      const uint4* x = reinterpret_cast<const uint4*>(bounds + static_cast<int64_t>(j) * 2 * D);
+      lo[i] = x[0];
+      hi[i] = x[D / E];
     }
   };
-  if (used > take) load(rank * kScoreBlocks);
+  if (used > take) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_one(rank * kScoreBlocks, i);
+  }
+  if (used > take && threadIdx.x < D) {
+    const T* q = static_cast<const T*>(p.q) + row * p.G * D + threadIdx.x;
+    double u = 0.0, d = 0.0;
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g) {
+      const float x = to_f32(q[g * D]);
+      // a NaN fails both comparisons and goes to both sums
+      u += x < 0.f ? 0.0 : static_cast<double>(x);
+      d += x > 0.f ? 0.0 : static_cast<double>(x);
+    }
+    up[threadIdx.x] = u;
+    down[threadIdx.x] = d;
+    up32[threadIdx.x] = static_cast<float>(u);
+    down32[threadIdx.x] = static_cast<float>(d);
+  }
   const bool renews = newest / kScoreBlocks % ctas == rank;
   if (renews) {
     const T* kn = static_cast<const T*>(p.k_new) + row * D + part * E;
@@ -609,21 +626,6 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
         hi[i] = x[D / E];
       }
   }
-  if (threadIdx.x < D) {
-    const T* q = static_cast<const T*>(p.q) + row * p.G * D + threadIdx.x;
-    double u = 0.0, d = 0.0;
-#pragma unroll 4
-    for (int g = 0; g < p.G; ++g) {
-      const float x = to_f32(q[g * D]);
-      // a NaN fails both comparisons and goes to both sums
-      u += x < 0.f ? 0.0 : static_cast<double>(x);
-      d += x > 0.f ? 0.0 : static_cast<double>(x);
-    }
-    up[threadIdx.x] = u;
-    down[threadIdx.x] = d;
-    up32[threadIdx.x] = static_cast<float>(u);
-    down32[threadIdx.x] = static_cast<float>(d);
-  }
   __syncthreads();
   float wu[E], wd[E];
 #pragma unroll
@@ -634,32 +636,48 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
   for (int j0 = rank * kScoreBlocks; j0 < used; j0 += ctas * kScoreBlocks) {
 #pragma unroll
     for (int i0 = 0; i0 < kIter; i0 += kAhead) {
-      float s[kAhead], a[kAhead];
+      // a thread's part of kAhead blocks' scores and magnitudes; the rows of the next
+      // blocks are asked for as these are used up
+      float v[2 * kAhead];
+      const int next = i0 + kAhead < kIter ? j0 + (i0 + kAhead) * kRows : j0 + ctas * kScoreBlocks;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        s[i] = a[i] = 0.f;
+        v[2 * i] = v[2 * i + 1] = 0.f;
         if (j0 + (i0 + i) * kRows + r < used) {
-          dot_piece<T>(lo[i], wd, s[i], a[i]);
-          dot_piece<T>(hi[i], wu, s[i], a[i]);
+          dot_piece<T>(lo[i], wd, v[2 * i], v[2 * i + 1]);
+          dot_piece<T>(hi[i], wu, v[2 * i], v[2 * i + 1]);
+        }
+        load_one(next, i);
+      }
+      // Summed over the row's lanes by halves: of n values a lane keeps the half that a bit
+      // of its number names, and adds its partner's.  All threads take part, with or
+      // without a block.
+      int mine = 0;
+#pragma unroll
+      for (int step = 0; step < kSteps; ++step) {
+        const int n = kAhead >> step, off = (kLanes / 2) >> step;
+        if (n > 0) {
+          const bool upper = part & off;
+          mine = 2 * mine + upper;
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            if (i < n) {
+              const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+              v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+            }
+        } else {
+          v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
         }
       }
-      load(i0 + kAhead < kIter ? j0 + (i0 + kAhead) * kRows : j0 + ctas * kScoreBlocks);
-      // all threads take part in the sums over a row's lanes, with or without a block
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) {
-          s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
-          a[i] += __shfl_xor_sync(0xffffffffu, a[i], off);
-        }
-        const int j = j0 + (i0 + i) * kRows + r;
-        const int back = newest >= j ? newest - j : newest - j + used;
-        if (part == 0 && j < used)
-          p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last)
-                                              ? ~0ull
-                                              : static_cast<uint64_t>(sortable(s[i])) << 32 |
-                                                    __float_as_uint(a[i] * kScoreError);
-      }
+      // this lane has value number `mine`: the score of block mine / 2, or its magnitudes
+      const float other = __shfl_xor_sync(0xffffffffu, v[0], kPair);
+      const int j = j0 + (i0 + mine / 2) * kRows + r;
+      const int back = newest >= j ? newest - j : newest - j + used;
+      if (!(part & (2 * kPair - 1)) && j < used)
+        p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last)
+                                            ? ~0ull
+                                            : static_cast<uint64_t>(sortable(v[0])) << 32 |
+                                                  __float_as_uint(other * kScoreError);
     }
   }
   if (ctas > 1) {
