@@ -5,8 +5,12 @@
 // Bound: device memory.  A row of D elements belongs to neighbouring lanes, 16 bytes of
 // the unquantised side each (so that a warp's accesses to it leave no sector half
 // done), whose largest magnitude is a few shuffles; a thread loads its part of
-// kRunRows rows before it works on the first.  The cache's slots are the rolling ones, position mod W, so a run may wrap
-// around its end.
+// kRunRows rows before it works on the first (of 2, 4, 8 and 16 rows, 8 were fastest: write
+// 16.5, 16.1, 15.4, 20.0 us; read 28.9, 27.5, 25.6, 28.3 us).  The cache's slots are the
+// rolling ones, position mod W, so a run may wrap around its end.
+// Measured at 8 KV heads of 128 in bf16: 15.4 us to write 8 runs of 614 to 2048 tokens (70 MB,
+// 4.5 TB/s: a fifth of the time is the start), 25.6 us to read 16 runs of 889 to 1777 (134 MB,
+// 5.2 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -13,6 +13,10 @@
 // the sines are formed, so that the loads are in flight meanwhile.  Angles are
 // formed in turns and reduced to half a turn in 64 bits (a position of 10^6 times
 // a rate of 1 has no fraction left in 32), the sine and cosine are taken in 32.
+// Divisions by the launch's sizes are products (fastdiv.cuh): with divide instructions
+// the bf16 kernel spent 79% of its issue slots and took 31 us for 32128 x 16 x 64.
+// Measured: 25 us there (132 MB, 5.2 TB/s), 29 us for 4099 x 40 x 128 in 32 bits (168 MB,
+// 5.8 TB/s), 2.6 us for 64 x 40 x 128.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
