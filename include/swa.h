@@ -381,7 +381,7 @@ swa_status swa_band_prefill(const void* q, const void* k, const void* v, void* o
  * One new token per sequence at position ``pos`` ([SWA]): its K/V is written into
  * the rolling cache at slot pos mod W, then q attends over the valid slots (all W
  * once pos >= W-1, else slots 0..pos).
- *   q, out: [B, Hq, head_dim]; k_new, v_new: [B, Hkv, head_dim];
+ *   q, out: [B, Hq, head_dim] (out may be q); k_new, v_new: [B, Hkv, head_dim];
  *   k_cache, v_cache: [B, W, Hkv, head_dim] (updated in place).
  *   workspace: device scratch of at least swa_decode_workspace_bytes(...) bytes
  *   (split-K partials); calls sharing a workspace must not overlap on the GPU.
@@ -471,7 +471,7 @@ swa_status swa_kv8_read(const void* k8, const uint8_t* k_exp, const void* v8, co
  * sequence, int64 in device memory: slots 0..min(pos[b], W-1) are valid.  pos[b] < 0
  * marks an idle row: its cache stays as it is, its output is zero.  A step can be
  * captured into a graph and replayed as pos, q, k_new and v_new change in place.
- *   q, out: [B, Hq, head_dim]; k_new, v_new: [B, Hkv, head_dim];
+ *   q, out: [B, Hq, head_dim] (out may be q); k_new, v_new: [B, Hkv, head_dim];
  *   caches [B, W, Hkv, head_dim], updated in place; other slots are not written, and
  *   slots behind the valid ones may hold anything, NaN included.
  *   workspace: device scratch of the matching _workspace_bytes (0 for sizes that the

@@ -544,6 +544,91 @@ def test_another_stream_and_a_workspace_of_the_callers(swa):
     assert e.value.status == -4
 
 
+def every_step(swa, B, W, Hq, Hkv, D, N, block, dtype, pos):
+    """The three steps on caches of their own: (name, step(q, kn, vn, out, **kw), workspace bytes, cache tensors)."""
+    k, v = randn((B, W, Hkv, D), 4, dtype), randn((B, W, Hkv, D), 5, dtype)
+    kp, vp = randn((N, Hkv, D), 6, dtype), randn((N, Hkv, D), 7, dtype)
+    c8, c1, c2 = new_cache8(B, W, Hkv, D), [k.clone(), v.clone()], [k.clone(), v.clone()]
+    swa.swa_kv8_write(k, v, *c8, torch.zeros_like(pos))
+    bounds = torch.zeros(B, Hkv, -(-W // block), 2, D, dtype=dtype, device="cuda")
+    swa.swa_block_bounds(k, pos - 1, bounds, block)
+    sel = torch.empty(B, Hkv, 5, dtype=torch.int32, device="cuda")
+    sizes = (B, Hq, Hkv, D, W)
+    return [
+        ("kv8", lambda q, kn, vn, out, **kw: swa.swa_decode_kv8(q, kn, vn, *c8, pos, out, **kw),
+         swa.swa_decode_kv8_workspace_bytes(*sizes), c8),
+        ("prefix", lambda q, kn, vn, out, **kw: swa.swa_decode_prefix(q, kn, vn, kp, vp, *c1, pos, out, **kw),
+         swa.swa_decode_prefix_workspace_bytes(*sizes, N), c1),
+        ("sparse", lambda q, kn, vn, out, **kw: swa.swa_decode_sparse(q, kn, vn, *c2, bounds, pos, out, sel, block, **kw),
+         swa.swa_decode_sparse_workspace_bytes(*sizes, block), c2 + [bounds]),
+    ]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_steps_whose_rows_are_all_idle(swa, dtype):
+    B, W, Hq, Hkv, D = 5, 90, 6, 2, 64
+    pos = torch.full((B,), -1, dtype=torch.int64, device="cuda")
+    q, kn, vn = (randn((B, h, D), s, dtype) for h, s in ((Hq, 1), (Hkv, 2), (Hkv, 3)))
+    for what, step, _, cache in every_step(swa, B, W, Hq, Hkv, D, 300, 16, dtype, pos):
+        before = [t.clone() for t in cache]
+        out = torch.full_like(q, float("nan"))
+        step(q, kn, vn, out)
+        assert not out.any(), what
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(cache, before)), what
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_output_in_place_of_the_queries(swa, dtype):
+    """`out` may be q: an item's queries are read before its output is written."""
+    B, W, Hq, Hkv, D = 7, 700, 12, 2, 64
+    pos = lengths(B, W, 8, idle=True).cuda()
+    q, kn, vn = (randn((B, h, D), s, dtype) for h, s in ((Hq, 1), (Hkv, 2), (Hkv, 3)))
+    for what, step, _, _ in every_step(swa, B, W, Hq, Hkv, D, 300, 16, dtype, pos):
+        out, here = torch.empty_like(q), q.clone()
+        step(q, kn, vn, out)
+        step(here, kn, vn, here)
+        assert torch.equal(here, out), what
+
+
+def test_steps_at_once_and_one_workspace_in_turn(swa):
+    """Steps on streams of their own with workspaces of their own overlap as they like; steps on one stream,
+    captured or not, may share one workspace, whatever kinds they are."""
+    B, W, Hq, Hkv, D, N, block = 9, 2000, 16, 4, 128, 900, 32
+    pos = lengths(B, W, 9).cuda()
+    q, kn, vn = (randn((B, h, D), s, BF16) for h, s in ((Hq, 1), (Hkv, 2), (Hkv, 3)))
+    steps = every_step(swa, B, W, Hq, Hkv, D, N, block, BF16, pos)
+    want = [torch.empty_like(q) for _ in steps]
+    for (_, step, _, _), o in zip(steps, want):
+        step(q, kn, vn, o)
+    streams = [torch.cuda.Stream() for _ in steps]
+    outs = [[torch.empty_like(q) for _ in range(20)] for _ in steps]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(20):
+        for (_, step, _, _), s, o in zip(steps, streams, outs):
+            with torch.cuda.stream(s):
+                step(q, kn, vn, o[i])
+    torch.cuda.synchronize()
+    for (what, _, _, _), w, o in zip(steps, want, outs):
+        assert all(torch.equal(w, x) for x in o), what
+    ws = torch.empty(max(n for _, _, n, _ in steps), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for (_, step, _, _), o in zip(steps, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step(q, kn, vn, o[0], workspace=ws)
+    for _ in range(3):
+        for g, (_, step, _, _), o in zip(graphs, steps, outs):
+            o[0].zero_()
+            o[1].zero_()
+            g.replay()
+            step(q, kn, vn, o[1], workspace=ws)
+    torch.cuda.synchronize()
+    for (what, _, _, _), w, o in zip(steps, want, outs):
+        assert torch.equal(w, o[0]) and torch.equal(w, o[1]), what
+    assert swa.swa_device_error_check() == 0
+
+
 def test_offsets_past_32_bits(swa):
     """The second sequence's rows begin past 2^31 elements (8-bit rows: bytes) of the cache."""
     B, W, Hkv, G, D = 2, 1_100_000, 8, 2, 128
