@@ -94,7 +94,16 @@ SWA_DEV int seq_places(const SeqParams& p, int n) {
 SWA_DEV int seq_tiles(const SeqParams& p, int n) { return (seq_places(p, n) + kSeqTile - 1) / kSeqTile; }
 
 // team that owns place t of the line of T >= teams: the c with c T / C <= t < (c + 1) T / C
-SWA_DEV int seq_owner(int64_t t, int64_t T, int teams) { return static_cast<int>(((t + 1) * teams - 1) / T); }
+SWA_DEV int seq_owner(int t, int T, int teams) {
+  // in 32 bits where they hold the product: 64-bit divisions are slow
+  if (T <= 0xffffffffu / kSeqMaxCtas) return static_cast<int>(((t + 1u) * teams - 1u) / static_cast<unsigned>(T));
+  return static_cast<int>(((t + 1ll) * teams - 1) / T);
+}
+// c T / C, for c <= C
+SWA_DEV int seq_ratio(int T, int c, int teams) {
+  if (T <= 0xffffffffu / kSeqMaxCtas) return static_cast<int>(static_cast<unsigned>(T) * c / teams);
+  return static_cast<int>(static_cast<int64_t>(T) * c / teams);
+}
 
 // A run of tiles of one sequence within a CTA's share.
 struct SeqRun {

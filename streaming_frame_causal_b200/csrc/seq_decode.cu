@@ -53,9 +53,13 @@ SWA_DEV int block_sum(int v, int& total) {
   return before;
 }
 
-// one block: every team's share of the line, and every sequence's teams
+// One block: every team's share of the line, and every sequence's teams.  The attention
+// waits for this: a search through the sequences in global memory is a chain of loads,
+// 0.3 us each, so those of up to kDivideKeep are searched in shared memory.
+constexpr int kDivideKeep = 1024;
 SWA_DEV void seq_divide(const SeqParams& p) {
-  // for now own[b] = {places, tiles} in front of sequence b
+  __shared__ int2 keep[kDivideKeep];
+  int2* at = p.B <= kDivideKeep ? keep : p.own;  // {places, tiles} in front of each sequence
   int T = 0, tiles = 0, n;
   for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
     const int b = b0 + threadIdx.x;
@@ -65,7 +69,7 @@ SWA_DEV void seq_divide(const SeqParams& p) {
     T += n;
     before.y = tiles + block_sum((mine + kSeqTile - 1) / kSeqTile, n);
     tiles += n;
-    if (b < p.B) p.own[b] = before;
+    if (b < p.B) at[b] = before;
   }
   __syncthreads();
   // no part is smaller than a tile, so that the pieces of a cut item are those of teams
@@ -79,16 +83,15 @@ SWA_DEV void seq_divide(const SeqParams& p) {
         lo = 0;  // the last b whose places begin at t or before it
         for (int hi = p.B; hi - lo > 1;) {
           const int mid = (lo + hi) >> 1;
-          if (p.own[mid].x <= t) lo = mid;
+          if (at[mid].x <= t) lo = mid;
           else hi = mid;
         }
-        return p.own[lo].y + max(0, t - p.own[lo].x - kSeqStart) / kSeqTile;
+        return at[lo].y + max(0, t - at[lo].x - kSeqStart) / kSeqTile;
       };
-      const int t = static_cast<int>(static_cast<int64_t>(T) * c / teams);
-      const int end = static_cast<int>(static_cast<int64_t>(T) * (c + 1) / teams);
+      const int t = seq_ratio(T, c, teams), end = seq_ratio(T, c + 1, teams);
       int other;
       const int first = find(t, s.x);
-      s.y = first - p.own[s.x].y;
+      s.y = first - at[s.x].y;
       s.z = (end < T ? find(end, other) : tiles) - first;
       s.w = seq_tokens(p, s.x);
     }
@@ -97,7 +100,7 @@ SWA_DEV void seq_divide(const SeqParams& p) {
   __syncthreads();
   for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
     // tile j is the last team's that begins at place 4 j + 3 of the sequence or before it
-    const int of = seq_places(p, seq_tokens(p, b)), t = p.own[b].x + kSeqStart;
+    const int of = seq_places(p, seq_tokens(p, b)), t = at[b].x + kSeqStart;
     int2 s = make_int2(0, 0);
     if (of > 0) {
       s.x = seq_owner(t + min(kSeqTile, of) - 1, T, teams);

@@ -218,6 +218,11 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     tmem_alloc(base + PL::kOffTmem, PL::kTmemCols);
     tmem_relinquish();
   }
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tp.tm_k);
+    tma_prefetch_desc(&tp.tm_v);
+    tma_prefetch_desc(&tp.tm_q);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -237,11 +242,6 @@ __global__ void __launch_bounds__(kThreads, SeqTcPlan<D, GP, KV8>::kPerSm)
     // the lanes issue the boxes of a tile side by side: of 32 rows, so that an item's
     // last tile brings few rows behind the keys, or of a selected block (8 of them at
     // most, 16 pieces)
-    if (lane == 0) {
-      tma_prefetch_desc(&tp.tm_k);
-      tma_prefetch_desc(&tp.tm_v);
-      tma_prefetch_desc(&tp.tm_q);
-    }
     const int rows = p.block ? p.block : kBoxRows;
     const int per_tile = kSeqKeys / rows;
     const int box = lane / PL::kSubs, sub = lane % PL::kSubs;
