@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/swa.h"
 #include "internal.h"
@@ -53,54 +54,75 @@ SWA_DEV int block_sum(int v, int& total) {
   return before;
 }
 
-// One block: every team's share of the line, and every sequence's teams.  The attention
-// waits for this: a search through the sequences in global memory is a chain of loads,
-// 0.3 us each, so those of up to kDivideKeep are searched in shared memory.
-constexpr int kDivideKeep = 1024;
+// One block: every team's share of the line, and every sequence's teams.  A search through
+// the sequences in global memory is a chain of loads, 0.3 us each.  seq_prep_kernel, which
+// the attention waits for, keeps them in shared memory where they are few (KEEP; not more
+// of it, as the attention's CTAs, which need most, start beside it); beside the scores of
+// blocks there is time.
+constexpr int kDivideKeep = 256;
+struct DivideMem {
+  int2 front[kDivideKeep];  // {places, tiles} in front of each sequence
+  int tokens[kDivideKeep];
+};
+
+template <bool KEEP>
 SWA_DEV void seq_divide(const SeqParams& p) {
-  __shared__ int2 keep[kDivideKeep];
-  int2* at = p.B <= kDivideKeep ? keep : p.own;  // {places, tiles} in front of each sequence
+  __shared__ std::conditional_t<KEEP, DivideMem, char> mem;
+  auto at = [&](int b) {
+    if constexpr (KEEP) return mem.front[b];
+    else return p.own[b];
+  };
+  auto tokens_of = [&](int b) {
+    if constexpr (KEEP) return mem.tokens[b];
+    else return seq_tokens(p, b);
+  };
   int T = 0, tiles = 0, n;
   for (int b0 = 0; b0 < p.B; b0 += kPrepThreads) {
     const int b = b0 + threadIdx.x;
-    const int mine = b < p.B ? seq_places(p, seq_tokens(p, b)) : 0;
+    const int have = b < p.B ? seq_tokens(p, b) : 0;
+    const int mine = seq_places(p, have);
     int2 before;
     before.x = T + block_sum(mine > 0 ? mine + kSeqStart : 0, n);
     T += n;
     before.y = tiles + block_sum((mine + kSeqTile - 1) / kSeqTile, n);
     tiles += n;
-    if (b < p.B) at[b] = before;
+    if (b < p.B) {
+      if constexpr (KEEP) {
+        mem.front[b] = before;
+        mem.tokens[b] = have;
+      } else {
+        p.own[b] = before;
+      }
+    }
   }
   __syncthreads();
   // no part is smaller than a tile, so that the pieces of a cut item are those of teams
   // that follow one another
   const int teams = min(p.teams, max(1, T / kSeqTile));
+  const int step = p.B > 1 ? 1 << (31 - __clz(p.B - 1)) : 0;
   for (int c = threadIdx.x; c < p.teams; c += kPrepThreads) {
     int4 s = make_int4(0, 0, 0, 0);
     if (c < teams && T > 0) {
-      // the sequence that holds place t < T, and the tiles that begin in front of t
-      auto find = [&](int t, int& lo) {
-        lo = 0;  // the last b whose places begin at t or before it
-        for (int hi = p.B; hi - lo > 1;) {
-          const int mid = (lo + hi) >> 1;
-          if (at[mid].x <= t) lo = mid;
-          else hi = mid;
-        }
-        return at[lo].y + max(0, t - at[lo].x - kSeqStart) / kSeqTile;
-      };
       const int t = seq_ratio(T, c, teams), end = seq_ratio(T, c + 1, teams);
-      int other;
-      const int first = find(t, s.x);
-      s.y = first - at[s.x].y;
-      s.z = (end < T ? find(end, other) : tiles) - first;
-      s.w = seq_tokens(p, s.x);
+      // the sequences that hold places t and end: the last that begin there or before
+      int lo = 0, hi = 0;
+      for (int i = step; i > 0; i >>= 1) {
+        if (lo + i < p.B && at(lo + i).x <= t) lo += i;
+        if (hi + i < p.B && at(hi + i).x <= end) hi += i;
+      }
+      // and the tiles that begin in front of the places
+      const int2 a = at(lo), z = at(hi);
+      s.x = lo;
+      s.y = max(0, t - a.x - kSeqStart) / kSeqTile;
+      s.z = (c + 1 < teams ? z.y + max(0, end - z.x - kSeqStart) / kSeqTile : tiles) - (a.y + s.y);
+      s.w = tokens_of(lo);
     }
     p.share[c] = s;
   }
   __syncthreads();
   for (int b = threadIdx.x; b < p.B; b += kPrepThreads) {
     // tile j is the last team's that begins at place 4 j + 3 of the sequence or before it
-    const int of = seq_places(p, seq_tokens(p, b)), t = at[b].x + kSeqStart;
+    const int of = seq_places(p, tokens_of(b)), t = at(b).x + kSeqStart;
     int2 s = make_int2(0, 0);
     if (of > 0) {
       s.x = seq_owner(t + min(kSeqTile, of) - 1, T, teams);
@@ -126,7 +148,8 @@ template <typename T, int D, int KIND>
 __global__ void __launch_bounds__(kPrepThreads) seq_prep_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
   if (blockIdx.x == 0) {
-    seq_divide(p);
+    if (p.B <= kDivideKeep) seq_divide<true>(p);
+    else seq_divide<false>(p);
     return;
   }
   constexpr int E = D / 32;  // elements of a lane
@@ -523,7 +546,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
   const int ctas = p.score_ctas, rank = blockIdx.x % ctas;
   const int64_t row = static_cast<int64_t>(blockIdx.x / ctas) - 1;
   if (row < 0) {
-    if (rank == 0) seq_divide(p);
+    if (rank == 0) seq_divide<false>(p);
     return;
   }
   const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<int64_t>(b) * p.Hkv);

@@ -544,6 +544,12 @@ def test_another_stream_and_a_workspace_of_the_callers(swa):
     assert e.value.status == -4
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_sequences_than_the_division_keeps_in_shared_memory(swa, dtype):
+    test_decode_kv8_matches_float64(swa, 700, 33, 2, 1, 64, dtype)
+    test_decode_prefix_matches_float64(swa, 257, 150, 2, 1, 64, dtype, 40)
+
+
 def every_step(swa, B, W, Hq, Hkv, D, N, block, dtype, pos):
     """The three steps on caches of their own: (name, step(q, kn, vn, out, **kw), workspace bytes, cache tensors)."""
     k, v = randn((B, W, Hkv, D), 4, dtype), randn((B, W, Hkv, D), 5, dtype)
