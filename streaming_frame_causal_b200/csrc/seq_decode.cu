@@ -407,7 +407,7 @@ SWA_DEV double exact_score(const T* bounds, const double* up, const double* down
 
 // The `take` best of `used` > take blocks, in ascending order.  score[j]: the sortable
 // 32-bit score in the upper half (all bits: a forced block) and the bound on its error in
-// the lower; bounds, up, down: what the scores are formed from.
+// the lower, in sm.keep where there is room; bounds, up, down: what the scores are formed from.
 template <typename T, int D>
 SWA_DEV void select_blocks(uint64_t* score, int used, int take, int* sel, const T* bounds, const double* up,
                            const double* down, SelectMem& sm) {
@@ -417,8 +417,7 @@ SWA_DEV void select_blocks(uint64_t* score, int used, int take, int* sel, const 
   int forced = 0;
   float err = 0.f;
   for (int j = threadIdx.x; j < used; j += kScoreThreads) {
-    const uint64_t s = __ldcg(reinterpret_cast<const unsigned long long*>(score + j));
-    if (kept) sm.keep[j] = s;
+    const uint64_t s = kept ? sm.keep[j] : __ldcg(reinterpret_cast<const unsigned long long*>(score + j));
     const float e = __uint_as_float(static_cast<uint32_t>(s));
     if (s >> 32 == kForced) ++forced;
     else err = e > err || isnan(e) ? e : err;  // a NaN stays
@@ -528,6 +527,20 @@ SWA_DEV void select_blocks(uint64_t* score, int used, int take, int* sel, const 
   }
 }
 
+SWA_DEV void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+SWA_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+SWA_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// v to the cluster's first CTA's shared memory, at what is addr in this one's
+SWA_DEV void st_first_cta(uint32_t addr, uint64_t v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u64 [a], %1;\n\t}" ::"r"(addr),
+      "l"(v)
+      : "memory");
+}
+
 // grid: a cluster for the division of the work, then one for each (sequence, KV head)
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __grid_constant__ SeqParams p) {
@@ -535,11 +548,13 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
   constexpr int E = 16 / sizeof(T);       // elements of a lane
   constexpr int kLanes = D / E;           // lanes of a row
   constexpr int kRows = kScoreThreads / kLanes;
+  constexpr int kStage = 4;               // keys of the token's block that a thread asks for ahead
+  __shared__ SelectMem select;
   __shared__ union {
+    uint4 stage[kStage][kScoreThreads];   // each thread's own
     struct {
       float low[kRows][D], high[kRows][D];
     } b;
-    SelectMem select;
   } sm;
   __shared__ double up[D], down[D];
   __shared__ __align__(16) float up32[D], down32[D];
@@ -550,7 +565,23 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
     return;
   }
   const int b = static_cast<int>(row / p.Hkv), h = static_cast<int>(row - static_cast<int64_t>(b) * p.Hkv);
-  const int n = seq_tokens(p, b);
+  const long long pos = p.pos[b];
+  if (threadIdx.x < D) {
+    const T* q = static_cast<const T*>(p.q) + row * p.G * D + threadIdx.x;
+    double u = 0.0, d = 0.0;
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g) {
+      const float x = to_f32(q[g * D]);
+      // a NaN fails both comparisons and goes to both sums
+      u += x < 0.f ? 0.0 : static_cast<double>(x);
+      d += x > 0.f ? 0.0 : static_cast<double>(x);
+    }
+    up[threadIdx.x] = u;
+    down[threadIdx.x] = d;
+    up32[threadIdx.x] = static_cast<float>(u);
+    down32[threadIdx.x] = static_cast<float>(d);
+  }
+  const int n = seq_tokens_at(p, pos);
   const int used = n > 0 ? (n + p.block - 1) / p.block : 0;
   const int take = min(used, p.n_select);
   int* sel = p.selected + row * p.n_select;
@@ -561,9 +592,25 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
       for (int i = threadIdx.x; i < used; i += kScoreThreads) sel[i] = i;
   }
   if (used == 0) return;
-  const int slot = static_cast<int>(p.pos[b] % p.W), newest = slot / p.block;
+  // scores go to the first CTA's shared memory, once it runs
+  const bool far = ctas > 1 && used > take, kept = used <= kSelKeep;
+  if (far) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int slot = static_cast<int>(pos % p.W), newest = slot / p.block;
   const int part = threadIdx.x % kLanes, r = threadIdx.x / kLanes;
-  // the rows of a thread's blocks first, so that they are on their way
+  // the keys of the token's block and the rows of a thread's first blocks are asked for
+  // first, so that they are on their way together
+  const bool renews = newest / kScoreBlocks % ctas == rank;
+  const int64_t step = static_cast<int64_t>(p.Hkv) * D;
+  const int end = min(newest * p.block + p.block, n);
+  T* k = static_cast<T*>(p.k_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + part * E;
+  if (renews) {
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+      const int s = newest * p.block + i * kRows + r;
+      if (s < end) cp_async16(&sm.stage[i][threadIdx.x], k + s * step);
+    }
+    cp_async_commit();
+  }
   constexpr int kIter = kScoreBlocks / kRows;
   constexpr int kAhead = kIter < 8 ? kIter : 8;
   static_assert(kIter % kAhead == 0 && 2 * kAhead <= kLanes, "whole rounds, a lane for every value");
@@ -583,42 +630,31 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load_one(rank * kScoreBlocks, i);
   }
-  if (used > take && threadIdx.x < D) {
-    const T* q = static_cast<const T*>(p.q) + row * p.G * D + threadIdx.x;
-    double u = 0.0, d = 0.0;
-#pragma unroll 4
-    for (int g = 0; g < p.G; ++g) {
-      const float x = to_f32(q[g * D]);
-      // a NaN fails both comparisons and goes to both sums
-      u += x < 0.f ? 0.0 : static_cast<double>(x);
-      d += x > 0.f ? 0.0 : static_cast<double>(x);
-    }
-    up[threadIdx.x] = u;
-    down[threadIdx.x] = d;
-    up32[threadIdx.x] = static_cast<float>(u);
-    down32[threadIdx.x] = static_cast<float>(d);
-  }
-  const bool renews = newest / kScoreBlocks % ctas == rank;
   if (renews) {
     const T* kn = static_cast<const T*>(p.k_new) + row * D + part * E;
     const T* vn = static_cast<const T*>(p.v_new) + row * D + part * E;
-    T* k = static_cast<T*>(p.k_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + part * E;
     T* v = static_cast<T*>(p.v_cache) + (static_cast<int64_t>(b) * p.W * p.Hkv + h) * D + part * E;
-    const int64_t step = static_cast<int64_t>(p.Hkv) * D;
     float least[E], most[E], x[E];
     load16(kn, x);
 #pragma unroll
     for (int i = 0; i < E; ++i) least[i] = most[i] = x[i];
-    const int end = min(newest * p.block + p.block, n);
-#pragma unroll 4
-    for (int s = newest * p.block + r; s < end; s += kRows) {
-      load16(s == slot ? kn : k + s * step, x);
+    auto widen = [&](const T* from) {
+      load16(from, x);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         least[i] = fminf(least[i], x[i]);
         most[i] = fmaxf(most[i], x[i]);
       }
-    }
+    };
+    cp_async_wait_all();
+    int s = newest * p.block + r;
+#pragma unroll
+    for (int i = 0; i < kStage; ++i, s += kRows)
+      if (s < end && s != slot) widen(reinterpret_cast<const T*>(&sm.stage[i][threadIdx.x]));
+#pragma unroll 4
+    for (; s < end; s += kRows)
+      if (s != slot) widen(k + s * step);
+    __syncthreads();
     if (r == 0) {
       *reinterpret_cast<uint4*>(k + slot * step) = *reinterpret_cast<const uint4*>(kn);
       *reinterpret_cast<uint4*>(v + slot * step) = *reinterpret_cast<const uint4*>(vn);
@@ -659,6 +695,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
     wu[i] = up32[part * E + i];
     wd[i] = down32[part * E + i];
   }
+  if (far) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   for (int j0 = rank * kScoreBlocks; j0 < used; j0 += ctas * kScoreBlocks) {
 #pragma unroll
     for (int i0 = 0; i0 < kIter; i0 += kAhead) {
@@ -699,11 +736,15 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
       const float other = __shfl_xor_sync(0xffffffffu, v[0], kPair);
       const int j = j0 + (i0 + mine / 2) * kRows + r;
       const int back = newest >= j ? newest - j : newest - j + used;
-      if (!(part & (2 * kPair - 1)) && j < used)
-        p.score[row * p.n_blocks + j] = (j < p.n_first || back < p.n_last)
-                                            ? ~0ull
-                                            : static_cast<uint64_t>(sortable(v[0])) << 32 |
-                                                  __float_as_uint(other * kScoreError);
+      if (!(part & (2 * kPair - 1)) && j < used) {
+        const uint64_t score = (j < p.n_first || back < p.n_last)
+                                   ? ~0ull
+                                   : static_cast<uint64_t>(sortable(v[0])) << 32 |
+                                         __float_as_uint(other * kScoreError);
+        if (!kept) p.score[row * p.n_blocks + j] = score;
+        else if (far) st_first_cta(smem_u32(&select.keep[j]), score);
+        else select.keep[j] = score;
+      }
     }
   }
   if (ctas > 1) {
@@ -713,7 +754,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
     __syncthreads();
   }
   select_blocks<T, D>(p.score + row * p.n_blocks, used, take, sel, static_cast<const T*>(p.bounds) + row * p.n_blocks * 2 * D,
-                      up, down, sm.select);
+                      up, down, select);
 }
 
 // ---------------------------------------------------------------- attention on CUDA cores
