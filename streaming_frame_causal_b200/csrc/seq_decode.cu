@@ -28,6 +28,16 @@ SWA_DEV float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 SWA_DEV void put_f32(float* p, float v) { *p = v; }
 SWA_DEV void put_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+SWA_DEV void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+SWA_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until at most N of the newest groups are on their way
+template <int N>
+SWA_DEV void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---------------------------------------------------------------- division and append
 constexpr int kPrepThreads = 256;
 constexpr int kPrepWarps = kPrepThreads / 32;
@@ -527,12 +537,6 @@ SWA_DEV void select_blocks(uint64_t* score, int used, int take, int* sel, const 
   }
 }
 
-SWA_DEV void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-SWA_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-SWA_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // v to the cluster's first CTA's shared memory, at what is addr in this one's
 SWA_DEV void st_first_cta(uint32_t addr, uint64_t v) {
   asm volatile(
@@ -646,7 +650,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
         most[i] = fmaxf(most[i], x[i]);
       }
     };
-    cp_async_wait_all();
+    cp_async_wait<0>();
     int s = newest * p.block + r;
 #pragma unroll
     for (int i = 0; i < kStage; ++i, s += kRows)
@@ -769,41 +773,57 @@ template <int D>
 struct SimtPlan {
   static constexpr int kLd = D + 4;
   static constexpr int kTile = kSeqKeys * kLd;
-  static constexpr int kFloats = kTile + kSeqRows * kSeqKeys + kSeqRows * D + 3 * kSeqRows + kSeqKeys;
+  static constexpr bool kTwo = D <= 64;  // keys and values in tiles of their own: three CTAs still fit an SM
+  static constexpr int kFloats = (kTwo ? 2 : 1) * kTile + kSeqRows * kSeqKeys + kSeqRows * D + 3 * kSeqRows + kSeqKeys;
   static constexpr int kSmem = kFloats * 4;
 };
 
-// rows [0, 128) of a tile: row r from slot[r] (-1, behind the keys: zeros), times 2^exp for 8-bit rows
+// Rows [0, 128) of a tile: row r from slot[r] (-1, behind the keys: zeros), times 2^exp for
+// 8-bit rows.  They are there once cp_async_wait has passed it.
 template <typename T, int D, int KIND>
 SWA_DEV void simt_load(float* tile, const void* rows, int64_t row_elems, const uint8_t* exps, const int* slots) {
-  constexpr int kParts = D / 8;
+  if constexpr (KIND == SEQ_PLAIN && sizeof(T) == 4) {  // as they are: not through registers
+    constexpr int kParts = D / 4;
 #pragma unroll 8
-  for (int i = threadIdx.x; i < kSeqKeys * kParts; i += kSimtThreads) {
-    const int r = i / kParts, part = i - r * kParts;
-    const int slot = slots[r];
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (slot >= 0) {
-      if constexpr (KIND == SEQ_KV8) {
-        const uint2 u =
-            *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(rows) + slot * row_elems + part * 8);
-        dequantise8(u, exps[slot] - 127, v);
-      } else {
-        load8(static_cast<const T*>(rows) + slot * row_elems + part * 8, v);
-      }
+    for (int i = threadIdx.x; i < kSeqKeys * kParts; i += kSimtThreads) {
+      const int r = i / kParts, part = i - r * kParts;
+      const int slot = slots[r];
+      float* dst = tile + r * SimtPlan<D>::kLd + part * 4;
+      if (slot >= 0) cp_async16(dst, static_cast<const T*>(rows) + slot * row_elems + part * 4);
+      else *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    store8(tile + r * SimtPlan<D>::kLd + part * 8, v);
+  } else {
+    constexpr int kParts = D / 8;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < kSeqKeys * kParts; i += kSimtThreads) {
+      const int r = i / kParts, part = i - r * kParts;
+      const int slot = slots[r];
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (slot >= 0) {
+        if constexpr (KIND == SEQ_KV8) {
+          const uint2 u =
+              *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(rows) + slot * row_elems + part * 8);
+          dequantise8(u, exps[slot] - 127, v);
+        } else {
+          load8(static_cast<const T*>(rows) + slot * row_elems + part * 8, v);
+        }
+      }
+      store8(tile + r * SimtPlan<D>::kLd + part * 8, v);
+    }
   }
+  cp_async_commit();
 }
 
 // the running state of one item's rows
 template <typename T, int D>
 struct SimtState {
   float acc[kSeqRows];
-  float *tile, *w, *q, *m, *l, *alpha;
+  float *tile, *values, *w, *q, *m, *l, *alpha;  // values: a tile of their own, or the keys'
   int* slots;  // of the tile's keys
   SWA_DEV void bind(float* smem) {
     tile = smem;
-    w = tile + SimtPlan<D>::kTile;
+    values = tile + (SimtPlan<D>::kTwo ? SimtPlan<D>::kTile : 0);
+    w = values + SimtPlan<D>::kTile;
     q = w + kSeqRows * kSeqKeys;
     m = q + kSeqRows * D;
     l = m + kSeqRows;
@@ -831,7 +851,9 @@ struct SimtState {
     const bool valid = slot >= 0;
     slots[r] = slot;
     __syncthreads();
-    load_k();
+    load_k(tile);
+    if (SimtPlan<D>::kTwo) load_v(values);
+    cp_async_wait<SimtPlan<D>::kTwo ? 1 : 0>();
     __syncthreads();
     float s[kSeqRows];
 #pragma unroll
@@ -848,7 +870,7 @@ struct SimtState {
 #pragma unroll
     for (int h = 0; h < kSeqRows; ++h) w[h * kSeqKeys + r] = valid ? s[h] * scale_log2 : -INFINITY;
     __syncthreads();
-    load_v();  // the keys are read
+    if (!SimtPlan<D>::kTwo) load_v(values);  // the keys are read
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       const int h = warp * 2 + hh;
@@ -879,16 +901,22 @@ struct SimtState {
         m[h] = m1;
       }
     }
+    cp_async_wait<0>();
     __syncthreads();
     constexpr int kParts = kSimtThreads / D;  // parts of the keys
     const int d = r % D, part = r / D;
 #pragma unroll
     for (int h = 0; h < kSeqRows; ++h) acc[h] *= alpha[h];
-#pragma unroll 4
-    for (int i = part * (kSeqKeys / kParts); i < (part + 1) * (kSeqKeys / kParts); ++i) {
-      const float v = tile[i * SimtPlan<D>::kLd + d];
+#pragma unroll 2
+    for (int i = part * (kSeqKeys / kParts); i < (part + 1) * (kSeqKeys / kParts); i += 4) {
+      float v[4];
 #pragma unroll
-      for (int h = 0; h < kSeqRows; ++h) acc[h] += w[h * kSeqKeys + i] * v;
+      for (int x = 0; x < 4; ++x) v[x] = values[(i + x) * SimtPlan<D>::kLd + d];
+#pragma unroll
+      for (int h = 0; h < kSeqRows; ++h) {
+        const float4 e = *reinterpret_cast<const float4*>(w + h * kSeqKeys + i);
+        acc[h] += e.x * v[0] + e.y * v[1] + e.z * v[2] + e.w * v[3];
+      }
     }
     __syncthreads();
   }
@@ -935,17 +963,21 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
   SeqRun run;
   while (walk.next(p, run)) {
     const int64_t qrow = static_cast<int64_t>(run.b) * p.Hq + kvh * p.G + g0;
+    // a tile's slots are loaded ahead of their use
+    int slot = seq_slot(p, run.b, kvh, run.tokens, run.t0, threadIdx.x);
     st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
     const int64_t row_elems = static_cast<int64_t>(p.Hkv) * D;
     const int64_t base = (static_cast<int64_t>(run.b) * p.W * p.Hkv + kvh) * D;
     const int64_t ebase = (static_cast<int64_t>(run.b) * p.Hkv + kvh) * p.W;
+    auto load = [&](float* tile, const void* cache, const uint8_t* exps) {
+      const uint8_t* rows8 = static_cast<const uint8_t*>(cache) + base * (KIND == SEQ_KV8 ? 1 : sizeof(T));
+      simt_load<T, D, KIND>(tile, rows8, row_elems, KIND == SEQ_KV8 ? exps + ebase : nullptr, st.slots);
+    };
     for (int t = run.t0; t < run.t0 + run.tiles; ++t) {
-      auto load = [&](const void* cache, const uint8_t* exps) {
-        const uint8_t* rows8 = static_cast<const uint8_t*>(cache) + base * (KIND == SEQ_KV8 ? 1 : sizeof(T));
-        simt_load<T, D, KIND>(st.tile, rows8, row_elems, KIND == SEQ_KV8 ? exps + ebase : nullptr, st.slots);
-      };
-      st.step(p.scale_log2, seq_slot(p, run.b, kvh, run.tokens, t, threadIdx.x), [&] { load(p.k_cache, p.k_exp); },
-              [&] { load(p.v_cache, p.v_exp); });
+      const int now = slot;
+      if (t + 1 < run.t0 + run.tiles) slot = seq_slot(p, run.b, kvh, run.tokens, t + 1, threadIdx.x);
+      st.step(p.scale_log2, now, [&](float* tile) { load(tile, p.k_cache, p.k_exp); },
+              [&](float* tile) { load(tile, p.v_cache, p.v_exp); });
     }
     st.end(rows, [&](int h, int d, float o, float m, float l) {
       if (run.slot < 0) {
@@ -1006,12 +1038,13 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
   const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits);
   st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
   for (int t = t0; t < t1; ++t) {
-    auto load = [&](const void* x) {
-      simt_load<T, D, SEQ_PLAIN>(st.tile, static_cast<const T*>(x) + kvh * D, static_cast<int64_t>(p.Hkv) * D, nullptr,
+    auto load = [&](float* tile, const void* x) {
+      simt_load<T, D, SEQ_PLAIN>(tile, static_cast<const T*>(x) + kvh * D, static_cast<int64_t>(p.Hkv) * D, nullptr,
                                  st.slots);
     };
     const int slot = t * kSeqKeys + static_cast<int>(threadIdx.x);
-    st.step(p.scale_log2, slot < p.N ? slot : -1, [&] { load(p.k_prefix); }, [&] { load(p.v_prefix); });
+    st.step(p.scale_log2, slot < p.N ? slot : -1, [&](float* tile) { load(tile, p.k_prefix); },
+            [&](float* tile) { load(tile, p.v_prefix); });
   }
   st.end(rows, [&](int h, int d, float o, float m, float l) {
     const int64_t at = static_cast<int64_t>(split) * p.B * p.Hq + qrow + h;
