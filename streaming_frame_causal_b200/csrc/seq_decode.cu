@@ -768,13 +768,14 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
 // heads for the softmax, a thread per output element (and 128 / D parts of the keys)
 // for the weighted sum.
 constexpr int kSimtThreads = 128;
+constexpr int kSimtPad = 4;
 
-template <int D>
+template <int D, int R>
 struct SimtPlan {
-  static constexpr int kLd = D + 4;
+  static constexpr int kLd = D + kSimtPad;
   static constexpr int kTile = kSeqKeys * kLd;
   static constexpr bool kTwo = D <= 64;  // keys and values in tiles of their own: three CTAs still fit an SM
-  static constexpr int kFloats = (kTwo ? 2 : 1) * kTile + kSeqRows * kSeqKeys + kSeqRows * D + 3 * kSeqRows + kSeqKeys;
+  static constexpr int kFloats = (kTwo ? 2 : 1) * kTile + R * kSeqKeys + R * D + 3 * R + kSeqKeys;
   static constexpr int kSmem = kFloats * 4;
 };
 
@@ -788,7 +789,7 @@ SWA_DEV void simt_load(float* tile, const void* rows, int64_t row_elems, const u
     for (int i = threadIdx.x; i < kSeqKeys * kParts; i += kSimtThreads) {
       const int r = i / kParts, part = i - r * kParts;
       const int slot = slots[r];
-      float* dst = tile + r * SimtPlan<D>::kLd + part * 4;
+      float* dst = tile + r * (D + kSimtPad) + part * 4;
       if (slot >= 0) cp_async16(dst, static_cast<const T*>(rows) + slot * row_elems + part * 4);
       else *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -808,41 +809,41 @@ SWA_DEV void simt_load(float* tile, const void* rows, int64_t row_elems, const u
           load8(static_cast<const T*>(rows) + slot * row_elems + part * 8, v);
         }
       }
-      store8(tile + r * SimtPlan<D>::kLd + part * 8, v);
+      store8(tile + r * (D + kSimtPad) + part * 8, v);
     }
   }
   cp_async_commit();
 }
 
-// the running state of one item's rows
-template <typename T, int D>
+// the running state of R rows of an item
+template <typename T, int D, int R>
 struct SimtState {
-  float acc[kSeqRows];
+  float acc[R];
   float *tile, *values, *w, *q, *m, *l, *alpha;  // values: a tile of their own, or the keys'
   int* slots;  // of the tile's keys
   SWA_DEV void bind(float* smem) {
     tile = smem;
-    values = tile + (SimtPlan<D>::kTwo ? SimtPlan<D>::kTile : 0);
-    w = values + SimtPlan<D>::kTile;
-    q = w + kSeqRows * kSeqKeys;
-    m = q + kSeqRows * D;
-    l = m + kSeqRows;
-    alpha = l + kSeqRows;
-    slots = reinterpret_cast<int*>(alpha + kSeqRows);
+    values = tile + (SimtPlan<D, R>::kTwo ? SimtPlan<D, R>::kTile : 0);
+    w = values + SimtPlan<D, R>::kTile;
+    q = w + R * kSeqKeys;
+    m = q + R * D;
+    l = m + R;
+    alpha = l + R;
+    slots = reinterpret_cast<int*>(alpha + R);
   }
   // q rows [0, rows) from src, the rest zero
   SWA_DEV void begin(const T* src, int rows) {
     __syncthreads();
-    for (int i = threadIdx.x; i < kSeqRows * D; i += kSimtThreads) {
+    for (int i = threadIdx.x; i < R * D; i += kSimtThreads) {
       const int r = i / D;
       q[i] = r < rows ? to_f32(src[i]) : 0.f;
     }
-    if (threadIdx.x < kSeqRows) {
+    if (threadIdx.x < R) {
       m[threadIdx.x] = -INFINITY;
       l[threadIdx.x] = 0.f;
     }
 #pragma unroll
-    for (int h = 0; h < kSeqRows; ++h) acc[h] = 0.f;
+    for (int h = 0; h < R; ++h) acc[h] = 0.f;
   }
   // one tile: keys, then values, loaded by the two functions
   template <typename LoadK, typename LoadV>
@@ -852,28 +853,27 @@ struct SimtState {
     slots[r] = slot;
     __syncthreads();
     load_k(tile);
-    if (SimtPlan<D>::kTwo) load_v(values);
-    cp_async_wait<SimtPlan<D>::kTwo ? 1 : 0>();
+    if (SimtPlan<D, R>::kTwo) load_v(values);
+    cp_async_wait<SimtPlan<D, R>::kTwo ? 1 : 0>();
     __syncthreads();
-    float s[kSeqRows];
+    float s[R];
 #pragma unroll
-    for (int h = 0; h < kSeqRows; ++h) s[h] = 0.f;
+    for (int h = 0; h < R; ++h) s[h] = 0.f;
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-      const float4 k = *reinterpret_cast<const float4*>(tile + r * SimtPlan<D>::kLd + d);
+      const float4 k = *reinterpret_cast<const float4*>(tile + r * SimtPlan<D, R>::kLd + d);
 #pragma unroll
-      for (int h = 0; h < kSeqRows; ++h) {
+      for (int h = 0; h < R; ++h) {
         const float4 x = *reinterpret_cast<const float4*>(q + h * D + d);
         s[h] += k.x * x.x + k.y * x.y + k.z * x.z + k.w * x.w;
       }
     }
 #pragma unroll
-    for (int h = 0; h < kSeqRows; ++h) w[h * kSeqKeys + r] = valid ? s[h] * scale_log2 : -INFINITY;
+    for (int h = 0; h < R; ++h) w[h * kSeqKeys + r] = valid ? s[h] * scale_log2 : -INFINITY;
     __syncthreads();
-    if (!SimtPlan<D>::kTwo) load_v(values);  // the keys are read
+    if (!SimtPlan<D, R>::kTwo) load_v(values);  // the keys are read
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int h = warp * 2 + hh;
+    for (int h = warp; h < R; h += kSimtThreads / 32) {
       float x[4], top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -906,14 +906,14 @@ struct SimtState {
     constexpr int kParts = kSimtThreads / D;  // parts of the keys
     const int d = r % D, part = r / D;
 #pragma unroll
-    for (int h = 0; h < kSeqRows; ++h) acc[h] *= alpha[h];
+    for (int h = 0; h < R; ++h) acc[h] *= alpha[h];
 #pragma unroll 2
     for (int i = part * (kSeqKeys / kParts); i < (part + 1) * (kSeqKeys / kParts); i += 4) {
       float v[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) v[x] = values[(i + x) * SimtPlan<D>::kLd + d];
+      for (int x = 0; x < 4; ++x) v[x] = values[(i + x) * SimtPlan<D, R>::kLd + d];
 #pragma unroll
-      for (int h = 0; h < kSeqRows; ++h) {
+      for (int h = 0; h < R; ++h) {
         const float4 e = *reinterpret_cast<const float4*>(w + h * kSeqKeys + i);
         acc[h] += e.x * v[0] + e.y * v[1] + e.z * v[2] + e.w * v[3];
       }
@@ -927,7 +927,7 @@ struct SimtState {
     const int d = threadIdx.x % D, part = threadIdx.x / D;
     if (kParts > 1) {
 #pragma unroll
-      for (int h = 0; h < kSeqRows; ++h) tile[(part * kSeqRows + h) * D + d] = acc[h];
+      for (int h = 0; h < R; ++h) tile[(part * R + h) * D + d] = acc[h];
       __syncthreads();
     }
     if (part == 0) {
@@ -935,10 +935,10 @@ struct SimtState {
         float o = acc[0];
         if (kParts > 1) {
           o = 0.f;
-          for (int i = 0; i < kParts; ++i) o += tile[(i * kSeqRows + h) * D + d];
+          for (int i = 0; i < kParts; ++i) o += tile[(i * R + h) * D + d];
         } else {
 #pragma unroll
-          for (int i = 1; i < kSeqRows; ++i)
+          for (int i = 1; i < R; ++i)
             if (i == h) o = acc[i];
         }
         put(h, d, o, m[h], l[h]);
@@ -947,18 +947,18 @@ struct SimtState {
   }
 };
 
-template <typename T, int D, int KIND>
+template <typename T, int D, int KIND, int R>
 __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_constant__ SeqParams p) {
   extern __shared__ __align__(16) float smem[];
   griddep_launch_dependents();
   griddep_wait();
-  SimtState<T, D> st;
+  SimtState<T, D, R> st;
   st.bind(smem);
   __shared__ int flag[2];
   SeqWalk walk;
   walk.start(p, blockIdx.x);
   const int kvh = walk.item / p.groups, g0 = (walk.item - kvh * p.groups) * kSeqRows;
-  const int rows = min(kSeqRows, p.G - g0);
+  const int rows = min(R, p.G - g0);
   int cut[2], n_cut = 0;  // sequences whose item this CTA holds a part of
   SeqRun run;
   while (walk.next(p, run)) {
@@ -1018,11 +1018,11 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
 }
 
 // the shared prefix: 8 of the batch's rows of a KV head against a piece of it
-template <typename T, int D>
+template <typename T, int D, int R>
 __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_constant__ SeqParams p) {
   extern __shared__ __align__(16) float smem[];
   griddep_launch_dependents();
-  SimtState<T, D> st;
+  SimtState<T, D, R> st;
   st.bind(smem);
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int64_t rg = blockIdx.x;  // (sequence, group of its heads)
@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
     griddep_wait();
     return;
   }
-  const int rows = min(kSeqRows, p.G - g0);
+  const int rows = min(R, p.G - g0);
   const int64_t qrow = static_cast<int64_t>(b) * p.Hq + kvh * p.G + g0;
   const int tiles = (p.N + kSeqKeys - 1) / kSeqKeys;
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
@@ -1196,6 +1196,17 @@ cudaError_t allow_smem(K kernel, int bytes, DeviceOnce& once) {
   return e;
 }
 
+// f(a constant: the rows that the CUDA-core kernels hold for groups of G query heads)
+template <typename F>
+cudaError_t with_rows(int G, F f) {
+  switch (seq_head_columns(std::min(G, kSeqRows))) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    default: return f(std::integral_constant<int, 8>());
+  }
+}
+
 template <typename T, int D, int KIND>
 cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
   constexpr bool kTc = sizeof(T) == 2;  // 16-bit queries: the tensor cores
@@ -1230,10 +1241,13 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
   if constexpr (kTc) {
     if (e == cudaSuccess) e = launch_seq_tc(p, D, KIND == SEQ_KV8, st);
   } else if (e == cudaSuccess) {
-    static DeviceOnce once;
-    e = allow_smem(seq_simt_kernel<T, D, KIND>, SimtPlan<D>::kSmem, once);
-    if (e == cudaSuccess)
-      e = launch_after(seq_simt_kernel<T, D, KIND>, dim3(p.ctas), dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
+    e = with_rows(p.G, [&](auto rows) {
+      constexpr int R = decltype(rows)::value;
+      static DeviceOnce once;
+      const cudaError_t a = allow_smem(seq_simt_kernel<T, D, KIND, R>, SimtPlan<D, R>::kSmem, once);
+      if (a != cudaSuccess) return a;
+      return launch_after(seq_simt_kernel<T, D, KIND, R>, dim3(p.ctas), dim3(kSimtThreads), SimtPlan<D, R>::kSmem, st, p);
+    });
     ++launches;
   }
   // The prefix's kernel needs nothing of the ones ahead of it, so it fills the SMs as
@@ -1244,11 +1258,14 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
         e = launch_prefix_tc(p.q, p.k_prefix, p.v_prefix, p.N, p.B, p.Hq, p.Hkv, D, p.splits, p.scale_log2, p.pre_o,
                              p.pre_ml, p.err, st);
       } else {
-        static DeviceOnce once;
-        e = allow_smem(prefix_simt_kernel<T, D>, SimtPlan<D>::kSmem, once);
         const dim3 grid(static_cast<unsigned>(p.B * p.groups), p.Hkv, p.splits);
-        if (e == cudaSuccess)
-          e = launch_after(prefix_simt_kernel<T, D>, grid, dim3(kSimtThreads), SimtPlan<D>::kSmem, st, p);
+        e = with_rows(p.G, [&](auto rows) {
+          constexpr int R = decltype(rows)::value;
+          static DeviceOnce once;
+          const cudaError_t a = allow_smem(prefix_simt_kernel<T, D, R>, SimtPlan<D, R>::kSmem, once);
+          if (a != cudaSuccess) return a;
+          return launch_after(prefix_simt_kernel<T, D, R>, grid, dim3(kSimtThreads), SimtPlan<D, R>::kSmem, st, p);
+        });
         ++launches;
       }
     }
