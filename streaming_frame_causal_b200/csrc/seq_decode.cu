@@ -762,74 +762,74 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
 }
 
 // ---------------------------------------------------------------- attention on CUDA cores
-// 32-bit queries and outputs.  One 128-key tile at a time in shared memory as 32-bit
-// values (rows D + 4 apart, so that eight lanes' 16-byte reads fall on different
-// banks): a thread per key for the scores of up to 8 query heads, a warp per two
-// heads for the softmax, a thread per output element (and 128 / D parts of the keys)
-// for the weighted sum.
+// 32-bit queries and outputs, R = 1, 2, 4 or 8 rows of an item at a time.  Tiles of 128 keys
+// go to shared memory as they are cached, past the registers (rows 16 bytes longer than
+// they need, so that eight lanes' 16-byte reads fall on different banks): a thread per
+// key for the scores, a warp per row for the softmax, a thread per 4 output elements and
+// 4 keys in every 512 / D for the weighted sum.  An 8-bit row's 2^e go to its score and to
+// its weight.  Bound by the latencies of a tile's phases, which 3 CTAs to an SM overlap.
+// Measured, 2 heads a group: 16 x 4096 x 8 x 64 in 54 us (268 MB, 5.0 TB/s), x 128 in 103
+// (537 MB, 5.2 TB/s); in 8 bits 34 us (68 MB) and 54 us (136 MB).
 constexpr int kSimtThreads = 128;
-constexpr int kSimtPad = 4;
 
-template <int D, int R>
+template <int D, int R, int KIND>
 struct SimtPlan {
-  static constexpr int kLd = D + kSimtPad;
+  static constexpr int kRow = D * (KIND == SEQ_KV8 ? 1 : 4);  // bytes of a cached row
+  static constexpr int kLd = kRow + 16;
   static constexpr int kTile = kSeqKeys * kLd;
-  static constexpr bool kTwo = D <= 64;  // keys and values in tiles of their own: three CTAs still fit an SM
-  static constexpr int kFloats = (kTwo ? 2 : 1) * kTile + R * kSeqKeys + R * D + 3 * R + kSeqKeys;
-  static constexpr int kSmem = kFloats * 4;
+  static constexpr int kParts = 4 * kSimtThreads / D;         // threads that share an output element
+  static constexpr bool kTwo = kRow <= 256;  // keys and values in tiles of their own: three CTAs still fit an SM
+  static constexpr int kSums = kParts * R * D * 4;            // their sums, in the tiles' place
+  static constexpr int kTiles = (kTwo ? 2 : 1) * kTile > kSums ? (kTwo ? 2 : 1) * kTile : kSums;
+  static constexpr int kSmem = kTiles + 4 * (R * kSeqKeys + R * D + 4 * R + 2 * kSeqKeys);
 };
 
-// Rows [0, 128) of a tile: row r from slot[r] (-1, behind the keys: zeros), times 2^exp for
-// 8-bit rows.  They are there once cp_async_wait has passed it.
-template <typename T, int D, int KIND>
-SWA_DEV void simt_load(float* tile, const void* rows, int64_t row_elems, const uint8_t* exps, const int* slots) {
-  if constexpr (KIND == SEQ_PLAIN && sizeof(T) == 4) {  // as they are: not through registers
-    constexpr int kParts = D / 4;
+// Rows [0, 128) of a tile: row r from slot[r] (-1, behind the keys: zeros).  They are
+// there once cp_async_wait has passed it.
+template <int ROW>
+SWA_DEV void simt_load(uint8_t* tile, const void* rows, int64_t row_bytes, const int* slots) {
+  constexpr int kPieces = ROW / 16;
 #pragma unroll 8
-    for (int i = threadIdx.x; i < kSeqKeys * kParts; i += kSimtThreads) {
-      const int r = i / kParts, part = i - r * kParts;
-      const int slot = slots[r];
-      float* dst = tile + r * (D + kSimtPad) + part * 4;
-      if (slot >= 0) cp_async16(dst, static_cast<const T*>(rows) + slot * row_elems + part * 4);
-      else *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  } else {
-    constexpr int kParts = D / 8;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < kSeqKeys * kParts; i += kSimtThreads) {
-      const int r = i / kParts, part = i - r * kParts;
-      const int slot = slots[r];
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (slot >= 0) {
-        if constexpr (KIND == SEQ_KV8) {
-          const uint2 u =
-              *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(rows) + slot * row_elems + part * 8);
-          dequantise8(u, exps[slot] - 127, v);
-        } else {
-          load8(static_cast<const T*>(rows) + slot * row_elems + part * 8, v);
-        }
-      }
-      store8(tile + r * (D + kSimtPad) + part * 8, v);
-    }
+  for (int i = threadIdx.x; i < kSeqKeys * kPieces; i += kSimtThreads) {
+    const int r = i / kPieces, piece = i - r * kPieces;
+    const int slot = slots[r];
+    uint8_t* dst = tile + r * (ROW + 16) + piece * 16;
+    if (slot >= 0) cp_async16(dst, static_cast<const uint8_t*>(rows) + slot * row_bytes + piece * 16);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
   }
   cp_async_commit();
 }
 
+// four elements of a row in shared memory
+template <int KIND>
+SWA_DEV float4 simt_four(const uint8_t* x) {
+  if constexpr (KIND == SEQ_KV8) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(x);
+    const float2 a = from_e4m3x2(u), b = from_e4m3x2(u >> 16);
+    return make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    return *reinterpret_cast<const float4*>(x);
+  }
+}
+
 // the running state of R rows of an item
-template <typename T, int D, int R>
+template <typename T, int D, int R, int KIND>
 struct SimtState {
-  float acc[R];
-  float *tile, *values, *w, *q, *m, *l, *alpha;  // values: a tile of their own, or the keys'
+  using PL = SimtPlan<D, R, KIND>;
+  float4 acc[R];
+  uint8_t *keys, *values;  // the values' tile may be the keys'
+  float *w, *q, *m, *l, *alpha, *scale;
   int* slots;  // of the tile's keys
-  SWA_DEV void bind(float* smem) {
-    tile = smem;
-    values = tile + (SimtPlan<D, R>::kTwo ? SimtPlan<D, R>::kTile : 0);
-    w = values + SimtPlan<D, R>::kTile;
+  SWA_DEV void bind(uint8_t* smem) {
+    keys = smem;
+    values = smem + (PL::kTwo ? PL::kTile : 0);
+    w = reinterpret_cast<float*>(smem + PL::kTiles);
     q = w + R * kSeqKeys;
-    m = q + R * D;
+    scale = q + R * D;  // 2^e of the values
+    slots = reinterpret_cast<int*>(scale + kSeqKeys);
+    m = reinterpret_cast<float*>(slots + kSeqKeys);
     l = m + R;
     alpha = l + R;
-    slots = reinterpret_cast<int*>(alpha + R);
   }
   // q rows [0, rows) from src, the rest zero
   SWA_DEV void begin(const T* src, int rows) {
@@ -843,35 +843,53 @@ struct SimtState {
       l[threadIdx.x] = 0.f;
     }
 #pragma unroll
-    for (int h = 0; h < R; ++h) acc[h] = 0.f;
+    for (int h = 0; h < R; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  // one tile: keys, then values, loaded by the two functions
+  // One tile: keys, then values, loaded by the two functions; this thread's key is in
+  // `slot`, and its rows are to be multiplied by k_scale and v_scale.
   template <typename LoadK, typename LoadV>
-  SWA_DEV void step(float scale_log2, int slot, LoadK load_k, LoadV load_v) {
+  SWA_DEV void step(float scale_log2, int slot, float k_scale, float v_scale, LoadK load_k, LoadV load_v) {
     const int r = threadIdx.x, warp = r >> 5, lane = r & 31;
     const bool valid = slot >= 0;
     slots[r] = slot;
+    if (KIND == SEQ_KV8) scale[r] = v_scale;
     __syncthreads();
-    load_k(tile);
-    if (SimtPlan<D, R>::kTwo) load_v(values);
-    cp_async_wait<SimtPlan<D, R>::kTwo ? 1 : 0>();
+    load_k(keys);
+    if (PL::kTwo) load_v(values);
+    cp_async_wait<PL::kTwo ? 1 : 0>();
     __syncthreads();
     float s[R];
 #pragma unroll
     for (int h = 0; h < R; ++h) s[h] = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-      const float4 k = *reinterpret_cast<const float4*>(tile + r * SimtPlan<D, R>::kLd + d);
+    const uint8_t* key = keys + r * PL::kLd;
+#pragma unroll 2
+    for (int d0 = 0; d0 < D; d0 += 16) {
+      float4 k[4];
+      if constexpr (KIND == SEQ_KV8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(key + d0);
+        const uint32_t word[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int h = 0; h < R; ++h) {
-        const float4 x = *reinterpret_cast<const float4*>(q + h * D + d);
-        s[h] += k.x * x.x + k.y * x.y + k.z * x.z + k.w * x.w;
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = from_e4m3x2(word[i]), c = from_e4m3x2(word[i] >> 16);
+          k[i] = make_float4(a.x, a.y, c.x, c.y);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = reinterpret_cast<const float4*>(key + d0 * 4)[i];
       }
+#pragma unroll
+      for (int h = 0; h < R; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(q + h * D + d0 + i * 4);
+          s[h] += k[i].x * x.x + k[i].y * x.y + k[i].z * x.z + k[i].w * x.w;
+        }
     }
 #pragma unroll
-    for (int h = 0; h < R; ++h) w[h * kSeqKeys + r] = valid ? s[h] * scale_log2 : -INFINITY;
+    for (int h = 0; h < R; ++h)
+      w[h * kSeqKeys + r] = valid ? (KIND == SEQ_KV8 ? s[h] * k_scale : s[h]) * scale_log2 : -INFINITY;
     __syncthreads();
-    if (!SimtPlan<D, R>::kTwo) load_v(values);  // the keys are read
+    if (!PL::kTwo) load_v(values);  // the keys are read
 #pragma unroll
     for (int h = warp; h < R; h += kSimtThreads / 32) {
       float x[4], top = -INFINITY;
@@ -888,7 +906,7 @@ struct SimtState {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float e = exp2f(x[i] - ref);
-        w[h * kSeqKeys + lane + 32 * i] = e;
+        w[h * kSeqKeys + lane + 32 * i] = KIND == SEQ_KV8 ? e * scale[lane + 32 * i] : e;
         sum += e;
       }
 #pragma unroll
@@ -903,19 +921,24 @@ struct SimtState {
     }
     cp_async_wait<0>();
     __syncthreads();
-    constexpr int kParts = kSimtThreads / D;  // parts of the keys
-    const int d = r % D, part = r / D;
+    const int d = r % (D / 4) * 4, part = r / (D / 4);
 #pragma unroll
-    for (int h = 0; h < R; ++h) acc[h] *= alpha[h];
+    for (int h = 0; h < R; ++h) {
+      const float a = alpha[h];
+      acc[h].x *= a; acc[h].y *= a; acc[h].z *= a; acc[h].w *= a;
+    }
 #pragma unroll 2
-    for (int i = part * (kSeqKeys / kParts); i < (part + 1) * (kSeqKeys / kParts); i += 4) {
-      float v[4];
+    for (int i = part * 4; i < kSeqKeys; i += 4 * PL::kParts) {
+      float4 v[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) v[x] = values[(i + x) * SimtPlan<D, R>::kLd + d];
+      for (int x = 0; x < 4; ++x) v[x] = simt_four<KIND>(values + (i + x) * PL::kLd + d * (PL::kRow / D));
 #pragma unroll
       for (int h = 0; h < R; ++h) {
         const float4 e = *reinterpret_cast<const float4*>(w + h * kSeqKeys + i);
-        acc[h] += e.x * v[0] + e.y * v[1] + e.z * v[2] + e.w * v[3];
+        acc[h].x += e.x * v[0].x + e.y * v[1].x + e.z * v[2].x + e.w * v[3].x;
+        acc[h].y += e.x * v[0].y + e.y * v[1].y + e.z * v[2].y + e.w * v[3].y;
+        acc[h].z += e.x * v[0].z + e.y * v[1].z + e.z * v[2].z + e.w * v[3].z;
+        acc[h].w += e.x * v[0].w + e.y * v[1].w + e.z * v[2].w + e.w * v[3].w;
       }
     }
     __syncthreads();
@@ -923,37 +946,28 @@ struct SimtState {
   // hands (head, element, sum over the keys, maximum, sum of the weights) to put
   template <typename Put>
   SWA_DEV void end(int rows, Put put) {
-    constexpr int kParts = kSimtThreads / D;
-    const int d = threadIdx.x % D, part = threadIdx.x / D;
-    if (kParts > 1) {
+    const int d = threadIdx.x % (D / 4) * 4, part = threadIdx.x / (D / 4);
+    float* sums = reinterpret_cast<float*>(keys);
 #pragma unroll
-      for (int h = 0; h < R; ++h) tile[(part * R + h) * D + d] = acc[h];
-      __syncthreads();
-    }
-    if (part == 0) {
-      for (int h = 0; h < rows; ++h) {
-        float o = acc[0];
-        if (kParts > 1) {
-          o = 0.f;
-          for (int i = 0; i < kParts; ++i) o += tile[(i * R + h) * D + d];
-        } else {
+    for (int h = 0; h < R; ++h) *reinterpret_cast<float4*>(sums + (part * R + h) * D + d) = acc[h];
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * D; i += kSimtThreads) {
+      float o = 0.f;
 #pragma unroll
-          for (int i = 1; i < R; ++i)
-            if (i == h) o = acc[i];
-        }
-        put(h, d, o, m[h], l[h]);
-      }
+      for (int x = 0; x < PL::kParts; ++x) o += sums[x * R * D + i];
+      const int h = i / D;
+      put(h, i - h * D, o, m[h], l[h]);
     }
   }
 };
 
 template <typename T, int D, int KIND, int R>
 __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_constant__ SeqParams p) {
-  extern __shared__ __align__(16) float smem[];
+  extern __shared__ __align__(16) uint8_t simt_smem[];
   griddep_launch_dependents();
   griddep_wait();
-  SimtState<T, D, R> st;
-  st.bind(smem);
+  SimtState<T, D, R, KIND> st;
+  st.bind(simt_smem);
   __shared__ int flag[2];
   SeqWalk walk;
   walk.start(p, blockIdx.x);
@@ -963,21 +977,30 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
   SeqRun run;
   while (walk.next(p, run)) {
     const int64_t qrow = static_cast<int64_t>(run.b) * p.Hq + kvh * p.G + g0;
-    // a tile's slots are loaded ahead of their use
-    int slot = seq_slot(p, run.b, kvh, run.tokens, run.t0, threadIdx.x);
-    st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
-    const int64_t row_elems = static_cast<int64_t>(p.Hkv) * D;
-    const int64_t base = (static_cast<int64_t>(run.b) * p.W * p.Hkv + kvh) * D;
+    const int64_t row_bytes = static_cast<int64_t>(p.Hkv) * SimtPlan<D, R, KIND>::kRow;
+    const int64_t base = static_cast<int64_t>(run.b) * p.W * row_bytes + kvh * SimtPlan<D, R, KIND>::kRow;
     const int64_t ebase = (static_cast<int64_t>(run.b) * p.Hkv + kvh) * p.W;
-    auto load = [&](float* tile, const void* cache, const uint8_t* exps) {
-      const uint8_t* rows8 = static_cast<const uint8_t*>(cache) + base * (KIND == SEQ_KV8 ? 1 : sizeof(T));
-      simt_load<T, D, KIND>(tile, rows8, row_elems, KIND == SEQ_KV8 ? exps + ebase : nullptr, st.slots);
+    // a tile's slots and exponents are loaded ahead of their use
+    int slot, ke = 127, ve = 127;
+    auto fetch = [&](int t) {
+      slot = seq_slot(p, run.b, kvh, run.tokens, t, threadIdx.x);
+      if constexpr (KIND == SEQ_KV8) {
+        ke = slot >= 0 ? p.k_exp[ebase + slot] : 127;
+        ve = slot >= 0 ? p.v_exp[ebase + slot] : 127;
+      }
+    };
+    fetch(run.t0);
+    st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
+    auto load = [&](uint8_t* tile, const void* cache) {
+      simt_load<SimtPlan<D, R, KIND>::kRow>(tile, static_cast<const uint8_t*>(cache) + base, row_bytes, st.slots);
     };
     for (int t = run.t0; t < run.t0 + run.tiles; ++t) {
       const int now = slot;
-      if (t + 1 < run.t0 + run.tiles) slot = seq_slot(p, run.b, kvh, run.tokens, t + 1, threadIdx.x);
-      st.step(p.scale_log2, now, [&](float* tile) { load(tile, p.k_cache, p.k_exp); },
-              [&](float* tile) { load(tile, p.v_cache, p.v_exp); });
+      const float k_scale = __uint_as_float(static_cast<uint32_t>(ke) << 23);
+      const float v_scale = __uint_as_float(static_cast<uint32_t>(ve) << 23);
+      if (t + 1 < run.t0 + run.tiles) fetch(t + 1);
+      st.step(p.scale_log2, now, k_scale, v_scale, [&](uint8_t* tile) { load(tile, p.k_cache); },
+              [&](uint8_t* tile) { load(tile, p.v_cache); });
     }
     st.end(rows, [&](int h, int d, float o, float m, float l) {
       if (run.slot < 0) {
@@ -1020,10 +1043,10 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
 // the shared prefix: 8 of the batch's rows of a KV head against a piece of it
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_constant__ SeqParams p) {
-  extern __shared__ __align__(16) float smem[];
+  extern __shared__ __align__(16) uint8_t simt_smem[];
   griddep_launch_dependents();
-  SimtState<T, D, R> st;
-  st.bind(smem);
+  SimtState<T, D, R, SEQ_PLAIN> st;
+  st.bind(simt_smem);
   const int kvh = blockIdx.y, split = blockIdx.z;
   const int64_t rg = blockIdx.x;  // (sequence, group of its heads)
   const int b = static_cast<int>(rg / p.groups), g0 = static_cast<int>(rg - static_cast<int64_t>(b) * p.groups) * kSeqRows;
@@ -1038,13 +1061,12 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
   const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits);
   st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
   for (int t = t0; t < t1; ++t) {
-    auto load = [&](float* tile, const void* x) {
-      simt_load<T, D, SEQ_PLAIN>(tile, static_cast<const T*>(x) + kvh * D, static_cast<int64_t>(p.Hkv) * D, nullptr,
-                                 st.slots);
+    auto load = [&](uint8_t* tile, const void* x) {
+      simt_load<D * 4>(tile, static_cast<const uint8_t*>(x) + kvh * D * 4, static_cast<int64_t>(p.Hkv) * D * 4, st.slots);
     };
     const int slot = t * kSeqKeys + static_cast<int>(threadIdx.x);
-    st.step(p.scale_log2, slot < p.N ? slot : -1, [&](float* tile) { load(tile, p.k_prefix); },
-            [&](float* tile) { load(tile, p.v_prefix); });
+    st.step(p.scale_log2, slot < p.N ? slot : -1, 1.f, 1.f, [&](uint8_t* tile) { load(tile, p.k_prefix); },
+            [&](uint8_t* tile) { load(tile, p.v_prefix); });
   }
   st.end(rows, [&](int h, int d, float o, float m, float l) {
     const int64_t at = static_cast<int64_t>(split) * p.B * p.Hq + qrow + h;
@@ -1244,9 +1266,10 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
     e = with_rows(p.G, [&](auto rows) {
       constexpr int R = decltype(rows)::value;
       static DeviceOnce once;
-      const cudaError_t a = allow_smem(seq_simt_kernel<T, D, KIND, R>, SimtPlan<D, R>::kSmem, once);
+      const cudaError_t a = allow_smem(seq_simt_kernel<T, D, KIND, R>, SimtPlan<D, R, KIND>::kSmem, once);
       if (a != cudaSuccess) return a;
-      return launch_after(seq_simt_kernel<T, D, KIND, R>, dim3(p.ctas), dim3(kSimtThreads), SimtPlan<D, R>::kSmem, st, p);
+      return launch_after(seq_simt_kernel<T, D, KIND, R>, dim3(p.ctas), dim3(kSimtThreads),
+                          SimtPlan<D, R, KIND>::kSmem, st, p);
     });
     ++launches;
   }
@@ -1262,9 +1285,9 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
         e = with_rows(p.G, [&](auto rows) {
           constexpr int R = decltype(rows)::value;
           static DeviceOnce once;
-          const cudaError_t a = allow_smem(prefix_simt_kernel<T, D, R>, SimtPlan<D, R>::kSmem, once);
+          const cudaError_t a = allow_smem(prefix_simt_kernel<T, D, R>, SimtPlan<D, R, SEQ_PLAIN>::kSmem, once);
           if (a != cudaSuccess) return a;
-          return launch_after(prefix_simt_kernel<T, D, R>, grid, dim3(kSimtThreads), SimtPlan<D, R>::kSmem, st, p);
+          return launch_after(prefix_simt_kernel<T, D, R>, grid, dim3(kSimtThreads), SimtPlan<D, R, SEQ_PLAIN>::kSmem, st, p);
         });
         ++launches;
       }
