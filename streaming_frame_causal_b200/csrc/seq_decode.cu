@@ -142,6 +142,12 @@ SWA_DEV void seq_divide(const SeqParams& p) {
   }
 }
 
+// sequences whose rows the CUDA cores take side by side against a shared prefix
+SWA_HD int prefix_span(const SeqParams& p) {
+  const int most = p.groups == 1 ? kSeqRows / p.G : 1;
+  return p.B < most ? p.B : most;
+}
+
 // One warp: nothing of the items of (sequence, KV head) row is done yet; an idle row's output
 template <typename T, int D>
 SWA_DEV void seq_start_row(const SeqParams& p, int64_t row, bool idle, int lane) {
@@ -767,9 +773,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
 // they need, so that eight lanes' 16-byte reads fall on different banks): a thread per
 // key for the scores, a warp per row for the softmax, a thread per 4 output elements and
 // 4 keys in every 512 / D for the weighted sum.  An 8-bit row's 2^e go to its score and to
-// its weight.  Bound by the latencies of a tile's phases, which 3 CTAs to an SM overlap.
+// its weight.  Bound by the latencies of a tile's phases, which 3 CTAs to an SM
+// (of 8-bit tiles 4) overlap.
 // Measured, 2 heads a group: 16 x 4096 x 8 x 64 in 54 us (268 MB, 5.0 TB/s), x 128 in 103
-// (537 MB, 5.2 TB/s); in 8 bits 34 us (68 MB) and 54 us (136 MB).
+// (537 MB, 5.2 TB/s); in 8 bits 33 us (68 MB) and 47 us (136 MB).
 constexpr int kSimtThreads = 128;
 
 template <int D, int R, int KIND>
@@ -831,12 +838,13 @@ struct SimtState {
     l = m + R;
     alpha = l + R;
   }
-  // q rows [0, rows) from src, the rest zero
-  SWA_DEV void begin(const T* src, int rows) {
+  // q rows [0, rows), row r from src(r), the rest zero
+  template <typename Src>
+  SWA_DEV void begin(int rows, Src src) {
     __syncthreads();
     for (int i = threadIdx.x; i < R * D; i += kSimtThreads) {
       const int r = i / D;
-      q[i] = r < rows ? to_f32(src[i]) : 0.f;
+      q[i] = r < rows ? to_f32(src(r)[i - r * D]) : 0.f;
     }
     if (threadIdx.x < R) {
       m[threadIdx.x] = -INFINITY;
@@ -990,7 +998,7 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
       }
     };
     fetch(run.t0);
-    st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
+    st.begin(rows, [&](int r) { return static_cast<const T*>(p.q) + (qrow + r) * D; });
     auto load = [&](uint8_t* tile, const void* cache) {
       simt_load<SimtPlan<D, R, KIND>::kRow>(tile, static_cast<const uint8_t*>(cache) + base, row_bytes, st.slots);
     };
@@ -1040,26 +1048,24 @@ __global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_con
   }
 }
 
-// the shared prefix: 8 of the batch's rows of a KV head against a piece of it
+// the shared prefix: up to 8 of the batch's rows of a KV head (whole groups of heads of
+// several sequences, or 8 heads of one) against a piece of it
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_constant__ SeqParams p) {
   extern __shared__ __align__(16) uint8_t simt_smem[];
   griddep_launch_dependents();
   SimtState<T, D, R, SEQ_PLAIN> st;
   st.bind(simt_smem);
-  const int kvh = blockIdx.y, split = blockIdx.z;
-  const int64_t rg = blockIdx.x;  // (sequence, group of its heads)
-  const int b = static_cast<int>(rg / p.groups), g0 = static_cast<int>(rg - static_cast<int64_t>(b) * p.groups) * kSeqRows;
-  if (p.pos[b] < 0) {
-    griddep_wait();
-    return;
-  }
-  const int rows = min(R, p.G - g0);
-  const int64_t qrow = static_cast<int64_t>(b) * p.Hq + kvh * p.G + g0;
+  const int kvh = blockIdx.y, split = blockIdx.z, rg = blockIdx.x;
+  const int span = prefix_span(p), b0 = rg / p.groups * span, g0 = rg % p.groups * kSeqRows;
+  const int rows = p.groups == 1 ? min(span, p.B - b0) * p.G : min(kSeqRows, p.G - g0);
+  auto row = [&](int r) {
+    return static_cast<int64_t>(b0 + (g0 + r) / p.G) * p.Hq + kvh * p.G + (g0 + r) % p.G;
+  };
   const int tiles = (p.N + kSeqKeys - 1) / kSeqKeys;
   const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.splits);
   const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.splits);
-  st.begin(static_cast<const T*>(p.q) + qrow * D, rows);
+  st.begin(rows, [&](int r) { return static_cast<const T*>(p.q) + row(r) * D; });
   for (int t = t0; t < t1; ++t) {
     auto load = [&](uint8_t* tile, const void* x) {
       simt_load<D * 4>(tile, static_cast<const uint8_t*>(x) + kvh * D * 4, static_cast<int64_t>(p.Hkv) * D * 4, st.slots);
@@ -1069,7 +1075,7 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
             [&](uint8_t* tile) { load(tile, p.v_prefix); });
   }
   st.end(rows, [&](int h, int d, float o, float m, float l) {
-    const int64_t at = static_cast<int64_t>(split) * p.B * p.Hq + qrow + h;
+    const int64_t at = static_cast<int64_t>(split) * p.B * p.Hq + row(h);
     p.pre_o[at * D + d] = o;
     if (d == 0) {
       p.pre_ml[at * 2] = m;
@@ -1148,7 +1154,7 @@ int prefix_pieces(const SeqParams& p, bool tc) {
   if (p.N == 0 || p.B == 0) return 0;
   const int tiles = cdiv(p.N, kSeqKeys), most = std::min(tiles, kSeqMaxSplits);
   if (!tc) {
-    const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.Hkv;
+    const int64_t ctas = static_cast<int64_t>(cdiv(p.B, prefix_span(p))) * p.groups * p.Hkv;
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((3 * 148 + ctas - 1) / ctas, most)));
   }
   const int64_t items = prefix_tc_items(p.B, p.G, p.Hkv);
@@ -1218,10 +1224,10 @@ cudaError_t allow_smem(K kernel, int bytes, DeviceOnce& once) {
   return e;
 }
 
-// f(a constant: the rows that the CUDA-core kernels hold for groups of G query heads)
+// f(a constant: the rows that the CUDA-core kernels hold for n query rows)
 template <typename F>
-cudaError_t with_rows(int G, F f) {
-  switch (seq_head_columns(std::min(G, kSeqRows))) {
+cudaError_t with_rows(int n, F f) {
+  switch (seq_head_columns(std::min(n, kSeqRows))) {
     case 1: return f(std::integral_constant<int, 1>());
     case 2: return f(std::integral_constant<int, 2>());
     case 4: return f(std::integral_constant<int, 4>());
@@ -1232,7 +1238,7 @@ cudaError_t with_rows(int G, F f) {
 template <typename T, int D, int KIND>
 cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
   constexpr bool kTc = sizeof(T) == 2;  // 16-bit queries: the tensor cores
-  const int ctas = kTc ? seq_tc_ctas(D, p.G, KIND == SEQ_KV8, device_sms()) : std::min(3 * device_sms(), kSeqMaxCtas);
+  const int ctas = kTc ? seq_tc_ctas(D, p.G, KIND == SEQ_KV8, device_sms()) : std::min((KIND == SEQ_KV8 ? 4 : 3) * device_sms(), kSeqMaxCtas);
   p.teams = std::max(1, ctas / p.items);
   p.ctas = p.teams * p.items;
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv;
@@ -1281,8 +1287,9 @@ cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
         e = launch_prefix_tc(p.q, p.k_prefix, p.v_prefix, p.N, p.B, p.Hq, p.Hkv, D, p.splits, p.scale_log2, p.pre_o,
                              p.pre_ml, p.err, st);
       } else {
-        const dim3 grid(static_cast<unsigned>(p.B * p.groups), p.Hkv, p.splits);
-        e = with_rows(p.G, [&](auto rows) {
+        const int span = prefix_span(p);
+        const dim3 grid(static_cast<unsigned>(cdiv(p.B, span) * p.groups), p.Hkv, p.splits);
+        e = with_rows(span * p.G, [&](auto rows) {
           constexpr int R = decltype(rows)::value;
           static DeviceOnce once;
           const cudaError_t a = allow_smem(prefix_simt_kernel<T, D, R>, SimtPlan<D, R, SEQ_PLAIN>::kSmem, once);
