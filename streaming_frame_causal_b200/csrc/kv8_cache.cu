@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kRunThreads) kv8_write_kernel(const __grid_con
   }
   uint8_t* x8 = (is_v ? p.x8[1] : p.x8[0]) + static_cast<int64_t>(b) * p.W * p.Hkv * D + at.part * P::kEl;
   uint8_t* exps = (is_v ? p.exp[1] : p.exp[0]) + static_cast<int64_t>(b) * p.Hkv * p.W;
-  const int slot0 = static_cast<int>((pos + skip) % p.W);
+  const int slot0 = static_cast<int>((pos % p.W + skip) % p.W);  // pos + skip may not fit 64 bits
 #pragma unroll
   for (int i = 0; i < kRunRows; ++i) {
     float v[P::kEl], a = 0.f;

@@ -175,6 +175,20 @@ def test_kv8_write_and_read_back(swa, B, T, W, Hkv, D, dtype):
             np.testing.assert_array_equal(np64(x), want)  # 4 significant bits and a power of two: exact in both
 
 
+def test_kv8_run_behind_the_last_position(swa):
+    """A run that is longer than the window and begins at the last 64-bit position."""
+    B, T, W, Hkv, D = 1, 13, 5, 2, 64
+    last = 2 ** 63 - 1
+    cache = new_cache8(B, W, Hkv, D)
+    k, v = randn((B, T, Hkv, D), 1, BF16), randn((B, T, Hkv, D), 2, BF16)
+    swa.swa_kv8_write(k, v, *cache, torch.tensor([last]).cuda())
+    for x, (x8, e) in ((k, cache[:2]), (v, cache[2:])):
+        val, ex = orc.quantise8(np64(x))
+        for t in range(T - W, T):
+            np.testing.assert_array_equal(np64(x8.float())[0, (last + t) % W], val[0, t])
+            np.testing.assert_array_equal(e.cpu().numpy()[0, :, (last + t) % W], ex[0, t] + 127)
+
+
 # ------------------------------------------------------------------ decode steps
 def lengths(B, W, seed, idle=False):
     g = np.random.RandomState(seed)
