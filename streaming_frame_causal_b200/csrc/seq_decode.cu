@@ -1160,12 +1160,16 @@ int prefix_pieces(const SeqParams& p, bool tc) {
   const int64_t items = prefix_tc_items(p.B, p.G, p.Hkv);
   int best = 1;
   double best_cost = 1e300;
-  for (int s = 1; s <= most; ++s) {
-    const double cost = static_cast<double>((items * s + 147) / 148) * (cdiv(tiles, s) + 7.5);
+  for (int64_t s = 1; s <= most;) {
+    // the most pieces for as many waves, and the fewest with as many tiles each
+    const int64_t waves = (items * s + 147) / 148, last = std::min<int64_t>(most, waves * 148 / items);
+    const int per = cdiv(tiles, static_cast<int>(last));
+    const double cost = static_cast<double>(waves) * (per + 7.5);
     if (cost < best_cost - 1e-9) {
       best_cost = cost;
-      best = s;
+      best = cdiv(tiles, per);
     }
+    s = last + 1;
   }
   return best;
 }
