@@ -383,7 +383,7 @@ def swa_rope_nd(x, pos, pairs, theta: float = 10000.0, inverse: bool = False, ou
     element pairs for axis a.  ``out`` may be x itself.  The gradient of the rotation
     is the call with ``inverse=True`` on the output's gradient (see include/swa.h)."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     axes = len(pairs)
     dev, (at,) = _fit(("pos", pos, x.shape[:-2] + (axes,), torch.int32))
     if out.shape != x.shape or out.dtype != x.dtype:
@@ -450,12 +450,16 @@ def swa_decode_sparse_workspace_bytes(B: int, Hq: int, Hkv: int, head_dim: int, 
 
 
 def _scratch(workspace, nbytes: int, like, dev: int, stream):
-    """The address and size of the step's workspace, allocated beside ``like`` if there is none."""
+    """The step's workspace, its address and size, allocated beside ``like`` if there is none."""
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=like.device)
-        if stream is not None:  # the memory may not be handed on before that stream is through with it
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream), device=like.device))
+        if stream is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=like.device)
+        else:
+            # from the memory of the stream that uses it: what another stream has freed may
+            # still be in use there, and this may be handed on only behind the step
+            own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), like.device)
+            with torch.cuda.stream(own):
+                workspace = torch.empty(max(nbytes, 16), dtype=_U8, device=like.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace: want a contiguous tensor on the device of the others")
     return workspace, workspace.data_ptr(), workspace.nbytes

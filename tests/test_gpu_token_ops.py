@@ -649,6 +649,30 @@ def test_steps_at_once_and_one_workspace_in_turn(swa):
     assert swa.swa_device_error_check() == 0
 
 
+def test_workspaces_of_steps_on_two_streams_are_apart(swa):
+    """A step on another stream, its workspace allocated in the call, beside steps on the current one whose
+    workspaces have been freed while they still run."""
+    B, W, Hq, Hkv, D = 16, 4096, 32, 8, 128
+    pos = torch.full((B,), W - 1, dtype=torch.int64, device="cuda")
+    q, kn, vn = (randn((B, h, D), s, BF16) for h, s in ((Hq, 1), (Hkv, 2), (Hkv, 3)))
+    steps = [every_step(swa, B, W, Hq, Hkv, D, 500, 64, BF16, pos)[0][1] for _ in range(2)]
+    want = [torch.empty_like(q) for _ in steps]
+    for step, o in zip(steps, want):
+        step(q, kn, vn, o)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(q) for _ in range(10)] for _ in steps]
+    for i in range(10):
+        steps[0](q, kn, vn, outs[0][i])
+        steps[1](q, kn, vn, outs[1][i], stream=side if i % 2 else side.cuda_stream)
+    torch.cuda.synchronize()
+    steps[0](q, kn, vn, outs[0][0].zero_(), stream=torch.cuda.current_stream().cuda_stream)
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+    assert swa.swa_device_error_check() == 0
+
+
 def test_offsets_past_32_bits(swa):
     """The second sequence's rows begin past 2^31 elements (8-bit rows: bytes) of the cache."""
     B, W, Hkv, G, D = 2, 1_100_000, 8, 2, 128
