@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   const int lane = threadIdx.x & 31;
   // a split stream attend's combine (programmatic launch) may launch now; it waits
   // for this grid before it reads a partial
-  griddep_launch_dependents();
+  // (the merge behind a prefix finds no room beside these CTAs: asked for early it only costs, 73.6
+  // against 72.5 us a call)
+  if constexpr (!PREFIX) griddep_launch_dependents();
 
   // barriers
   const uint32_t bar0 = base + PL::kOffBar;
