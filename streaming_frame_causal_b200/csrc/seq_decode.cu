@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) block_score_kernel(const __g
 // its weight.  Bound by the latencies of a tile's phases, which 3 CTAs to an SM
 // (of 8-bit tiles 4) overlap.
 // Measured, 2 heads a group: 16 x 4096 x 8 x 64 in 54 us (268 MB, 5.0 TB/s), x 128 in 103
-// (537 MB, 5.2 TB/s); in 8 bits 33 us (68 MB) and 47 us (136 MB).
+// (537 MB, 5.2 TB/s); in 8 bits 29 us (68 MB) and 46 us (136 MB).
 constexpr int kSimtThreads = 128;
 
 template <int D, int R, int KIND>
@@ -788,7 +788,10 @@ struct SimtPlan {
   static constexpr bool kTwo = kRow <= 256;  // keys and values in tiles of their own: three CTAs still fit an SM
   static constexpr int kSums = kParts * R * D * 4;            // their sums, in the tiles' place
   static constexpr int kTiles = (kTwo ? 2 : 1) * kTile > kSums ? (kTwo ? 2 : 1) * kTile : kSums;
-  static constexpr int kSmem = kTiles + 4 * (R * kSeqKeys + R * D + 4 * R + 2 * kSeqKeys);
+  static constexpr int kScales = KIND == SEQ_KV8 ? kSeqKeys : 0;
+  static constexpr int kSmem = kTiles + 4 * (R * kSeqKeys + R * D + 3 * R + kSeqKeys + kScales);
+  static constexpr int kPerSm = KIND == SEQ_KV8 ? 4 : 3;      // CTAs
+  static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "an SM holds them");
 };
 
 // Rows [0, 128) of a tile: row r from slot[r] (-1, behind the keys: zeros).  They are
@@ -833,7 +836,7 @@ struct SimtState {
     w = reinterpret_cast<float*>(smem + PL::kTiles);
     q = w + R * kSeqKeys;
     scale = q + R * D;  // 2^e of the values
-    slots = reinterpret_cast<int*>(scale + kSeqKeys);
+    slots = reinterpret_cast<int*>(scale + PL::kScales);
     m = reinterpret_cast<float*>(slots + kSeqKeys);
     l = m + R;
     alpha = l + R;
@@ -970,7 +973,8 @@ struct SimtState {
 };
 
 template <typename T, int D, int KIND, int R>
-__global__ void __launch_bounds__(kSimtThreads) seq_simt_kernel(const __grid_constant__ SeqParams p) {
+__global__ void __launch_bounds__(kSimtThreads, SimtPlan<D, R, KIND>::kPerSm)
+    seq_simt_kernel(const __grid_constant__ SeqParams p) {
   extern __shared__ __align__(16) uint8_t simt_smem[];
   griddep_launch_dependents();
   griddep_wait();
@@ -1242,7 +1246,8 @@ cudaError_t with_rows(int n, F f) {
 template <typename T, int D, int KIND>
 cudaError_t launch_step(SeqParams& p, cudaStream_t st) {
   constexpr bool kTc = sizeof(T) == 2;  // 16-bit queries: the tensor cores
-  const int ctas = kTc ? seq_tc_ctas(D, p.G, KIND == SEQ_KV8, device_sms()) : std::min((KIND == SEQ_KV8 ? 4 : 3) * device_sms(), kSeqMaxCtas);
+  const int ctas = kTc ? seq_tc_ctas(D, p.G, KIND == SEQ_KV8, device_sms())
+                       : std::min(SimtPlan<D, 1, KIND>::kPerSm * device_sms(), kSeqMaxCtas);
   p.teams = std::max(1, ctas / p.items);
   p.ctas = p.teams * p.items;
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hkv;
