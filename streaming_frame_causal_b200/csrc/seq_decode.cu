@@ -286,7 +286,9 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const SeqParams p) {
 // Bound: the bounds' bytes.  The CTAs of a cluster take 128 blocks of one (sequence, KV
 // head) in turn, lanes 16 bytes of a row each; the CTA that has the token's
 // block first renews its bounds from all its valid keys (the slot's old key may have
-// been one of the extremes).  When all have finished, the first CTA selects.
+// been one of the extremes).  Scores go to the first CTA's shared memory; when all are
+// there it selects.  Measured for 16 x 8 rows of 256 to 512 blocks of 128 elements (27 MB):
+// scores after 7 to 9 us, selections after 12 to 15.
 constexpr int kScoreThreads = kPrepThreads;
 constexpr int kScoreBlocks = 128; // cache blocks of a CTA at a time
 constexpr int kScoreCtas = 8;     // CTAs of a row at most (a cluster)
@@ -1092,7 +1094,8 @@ __global__ void __launch_bounds__(kSimtThreads) prefix_simt_kernel(const __grid_
 
 // ---------------------------------------------------------------- merge with the prefix
 // The pieces of every (sequence, query head): those of its item in the order of the
-// tiles, then the prefix's; one warp, or up to 8 where there are many.
+// tiles, then the prefix's; one warp, or up to 8 where there are many.  Bound by the
+// latency of its loads: 7 us for 2048 rows of 19 to 21 pieces of 128 (21 MB in L2).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(const __grid_constant__ SeqParams p) {
   griddep_launch_dependents();
